@@ -350,6 +350,175 @@ QUIK_API quik_status quik_linear_noalloc(const quik_shape *shape, const void *X_
                                          void *Y_f16, quik_stream_t stream);
 
 /*
+ * The attention between a layer's QKV projection and its output projection
+ * (Atom summary: the KV cache is quantised to low bits as well; the pages
+ * give no layout, so the layouts below are this library's).
+ *
+ * A head is head_dim = 64 or 128 consecutive fp16 channels; a token's heads
+ * follow one another.  Row strides are in elements, a multiple of 8 and at
+ * least heads * head_dim, so q, k and v may be read in place from the rows
+ * [q heads | k heads | v heads] that one projection writes.
+ *
+ * Rotation: of each head the first rotary_dim channels (0: none; a multiple
+ * of 16, at most head_dim) are turned in pairs,
+ *     (a, b) -> (a cos - b sin, b cos + a sin),
+ * pair i being channels (i, i + rotary_dim / 2), or with `interleaved`
+ * channels (2i, 2i + 1).  cos_table and sin_table are fp32
+ * [table_rows, rotary_dim / 2]; token t uses row positions[t].  A position
+ * outside [0, table_rows) is never used as an address: it reads row 0, is
+ * counted, and quik_sync_check reports QUIK_ERR_INVALID_ARG.
+ *
+ * All entry points below follow the conventions above (asynchronous,
+ * validated before any launch; device pointers 16-byte aligned, those to
+ * positions, slots, page tables, lengths, masks and lse by their element),
+ * launch on the current device, and return QUIK_OK without a launch when there
+ * are no tokens.  Another head_dim, or more than 4096 heads, is
+ * QUIK_ERR_UNSUPPORTED.
+ */
+typedef struct {
+    int32_t tokens;      /* rows, >= 0 */
+    int32_t q_heads;     /* query heads (quik_kv_append: not used) */
+    int32_t kv_heads;    /* key (and value) heads */
+    int32_t head_dim;    /* 64 or 128 */
+    int32_t rotary_dim;  /* channels rotated in each head; 0: no rotation (tables may be NULL) */
+    int32_t interleaved; /* 0: pairs (i, i + rotary_dim / 2); 1: pairs (2i, 2i + 1) */
+    int32_t table_rows;  /* rows of the cos / sin tables */
+} quik_heads;
+
+/*
+ * quik_qk_norm_rope -- the RMS norm of each query and key head with the
+ * rotation in the same pass:
+ *     y = x * r * gamma,  r = 1 / sqrt(mean(x^2) + eps) over the head,
+ * then the rotation, in fp32, rounded once to fp16.
+ *   q [tokens, q_heads, head_dim], k [tokens, kv_heads, head_dim] fp16 with
+ *   row strides q_stride, k_stride; q_gamma, k_gamma fp16 [head_dim] or NULL
+ *   (no norm); eps finite and > 0 where either is given.
+ *   q_out, k_out: as q and k; each may be its input (same stride), and must
+ *   not overlap it otherwise.  q_heads or kv_heads may be 0 (its pointers are
+ *   then not used), not both.
+ */
+QUIK_API quik_status quik_qk_norm_rope(const quik_heads *heads, const void *q, int64_t q_stride,
+                                       const void *k, int64_t k_stride, const void *q_gamma,
+                                       const void *k_gamma, float eps, const float *cos_table,
+                                       const float *sin_table, const int32_t *positions,
+                                       void *q_out, int64_t q_out_stride, void *k_out,
+                                       int64_t k_out_stride, quik_stream_t stream);
+
+typedef enum {
+    QUIK_KV_FP16 = 0,
+    QUIK_KV_INT8 = 1, /* int8 codes, one fp32 scale per row: max|v| / 127 */
+    QUIK_KV_INT4 = 2  /* packed INT4 codes (the byte layout above), max|v| / 7 */
+} quik_kv_t;
+
+/*
+ * A paged KV cache: k and v [pages, heads, page_size, row] with row = head_dim
+ * fp16 values, int8 codes, or head_dim / 2 bytes of packed INT4;
+ * k_scale and v_scale fp32 [pages, heads, page_size] (quantised types only).
+ * A row is one head of one token, quantised by the library's rule
+ * (s = max / 127 or / 7, q = clamp(rint(v / s)), a zero row has s = 0).  A row
+ * that holds an infinity or a NaN has it as its scale and stands for NaN.
+ * Slot s is token s % page_size of page s / page_size.  page_size is a power
+ * of two from 16 to 256.  Offsets are 64-bit: the pool may be of any size.
+ */
+typedef struct {
+    int32_t kv_type;   /* a quik_kv_t */
+    int32_t heads;     /* key / value heads */
+    int32_t head_dim;  /* 64 or 128 */
+    int32_t page_size; /* 16, 32, 64, 128 or 256 */
+    int32_t pages;     /* >= 1 */
+    int32_t reserved;  /* 0 */
+    void *k, *v;
+    float *k_scale, *v_scale;
+} quik_kv_cache;
+
+/*
+ * quik_kv_append -- write the rows of `tokens` tokens into the cache, the keys
+ * rotated on the way (rotary_dim 0: as they are).  The rotation is taken in
+ * fp32, each product and each sum rounded (IEEE); FP16 rows are rounded once
+ * to fp16, codes and scales are those of the fp32 values, bit for bit.
+ *   heads: tokens, kv_heads (the cache's), head_dim (the cache's), rotation
+ *   k, v [tokens, heads, head_dim] fp16 with row strides
+ *   slots int64 [tokens]: token t's slot.  Negative: the token is left out
+ *   (padding).  A slot past the cache is not written, is counted, and
+ *   quik_sync_check reports QUIK_ERR_INVALID_ARG.  Slots of one call must
+ *   differ (a slot named twice holds a mixture of its rows).
+ */
+QUIK_API quik_status quik_kv_append(const quik_heads *heads, const quik_kv_cache *cache,
+                                    const void *k, int64_t k_stride, const void *v,
+                                    int64_t v_stride, const float *cos_table,
+                                    const float *sin_table, const int32_t *positions,
+                                    const int64_t *slots, quik_stream_t stream);
+
+/*
+ * quik_kv_gather -- the rows of `tokens` slots as fp16 (code * scale in fp32,
+ * rounded once): a prefix for dense attention, or for another cache.
+ * k_out, v_out [tokens, heads, head_dim] with row strides; a negative slot
+ * gives zeros, a slot past the cache gives zeros and is counted as above.
+ */
+QUIK_API quik_status quik_kv_gather(const quik_kv_cache *cache, int32_t tokens,
+                                    const int64_t *slots, void *k_out, int64_t k_stride,
+                                    void *v_out, int64_t v_stride, quik_stream_t stream);
+
+/*
+ * quik_tree_attention -- attention of drafted tokens over the cache: one token
+ * of each sequence (decoding), a tree of drafted tokens to be verified, or a
+ * chunk of a prompt.
+ *
+ * Sequence b has context[b] tokens in the cache and then its own
+ * n_b = cu_tokens[b + 1] - cu_tokens[b] new tokens, whose rows have been
+ * appended already: new token i is at position context[b] + i, position p in
+ * page page_table[b, p / page_size].  Row cu_tokens[b] + i of q sees every
+ * context token, and new token j where bit j % 32 of word j / 32 of its row
+ * of tree_mask is set (its ancestors and, normally, itself).  tree_mask NULL:
+ * a chain, j <= i.  For query head h, with key head h / (q_heads / kv heads):
+ *     out = sum_j p_j v_j,  p = softmax over the visible j of scale * (q . k_j)
+ *     lse = ln sum_j exp(scale * (q . k_j))
+ * Scores, softmax and sums are fp32; p is rounded to fp16 before its product
+ * with the stored values (codes, in the quantised types: the values' scale is
+ * part of p then).  A row that sees nothing gives zeros and lse = -infinity.
+ * A token that a row does not see has no influence on it, whatever its cache
+ * row holds.
+ *   q [tokens, q_heads, head_dim] fp16, row stride q_stride; out alike
+ *   page_table int32 [sequences, max_pages]; context int32 [sequences];
+ *   cu_tokens int32 [sequences + 1], ascending from >= 0 to <= tokens
+ *   tree_mask uint32 [tokens, mask_words], mask_words >= max_tokens / 32
+ *   rounded up (NULL: mask_words is not used)
+ *   lse fp32 [tokens, q_heads] or NULL
+ *   max_tokens: the largest n_b; max_context: the largest context[b], a hint
+ *   that only chooses how the work is split (any value is right)
+ * Rows of out and lse before cu_tokens[0] and from cu_tokens[sequences] on
+ * are left as they were.  Positions are read in place: a page number outside
+ * [0, pages) is never used as an address (its tokens are unseen), a sequence
+ * longer than its page table is cut to it, an n_b that is negative, larger
+ * than max_tokens or past `tokens` leaves that sequence's rows unwritten; all
+ * are counted and quik_sync_check reports QUIK_ERR_INVALID_ARG.
+ *   workspace: quik_attention_workspace_size bytes (may be NULL when that is
+ *   0), the caller's; two calls that may overlap on the GPU need one each.
+ */
+typedef struct {
+    int32_t tokens;      /* rows of q and out */
+    int32_t sequences;
+    int32_t q_heads;     /* a multiple of the cache's heads */
+    int32_t max_tokens;  /* largest number of new tokens of a sequence */
+    int32_t max_pages;   /* columns of page_table */
+    int32_t max_context; /* largest context (a hint) */
+    int32_t mask_words;  /* words of a row of tree_mask */
+    float scale;         /* finite */
+} quik_attention;
+
+/* Bytes of workspace (0: none needed, or arguments that the call rejects). */
+QUIK_API size_t quik_attention_workspace_size(const quik_attention *attention,
+                                              const quik_kv_cache *cache);
+
+QUIK_API quik_status quik_tree_attention(const quik_attention *attention,
+                                         const quik_kv_cache *cache, const void *q,
+                                         int64_t q_stride, const int32_t *page_table,
+                                         const int32_t *context, const int32_t *cu_tokens,
+                                         const uint32_t *tree_mask, void *out, int64_t out_stride,
+                                         float *lse, void *workspace, size_t workspace_bytes,
+                                         quik_stream_t stream);
+
+/*
  * quik_gemm_i32_debug -- test entry: the exact integer sums of the INT4 part
  * as computed by the tensor-core main loop, acc [M, N] int32 (or [G, M, N]
  * with groups), and for INT8 outliers the outlier block's integer sums
@@ -363,11 +532,11 @@ QUIK_API quik_status quik_gemm_i32_debug(const quik_shape *shape, const void *Xq
  * quik_sync_check -- synchronise `stream`, then report the device error
  * counters of the current device: QUIK_ERR_TIMEOUT if a bounded wait ran out
  * in any kernel since the previous check, else QUIK_ERR_INVALID_ARG if a
- * quantiser met a perm entry outside [0, K) since then, QUIK_ERR_CUDA on a
- * CUDA error, else QUIK_OK.  The counters are never reset on the device (a
- * kernel running on another stream meanwhile is not disturbed); each check
- * reports what was added since the previous one, whichever stream it came
- * from.
+ * quantiser met a perm entry outside [0, K), or one of the attention's kernels
+ * an index out of range, since then, QUIK_ERR_CUDA on a CUDA error, else
+ * QUIK_OK.  The counters are never reset on the device (a kernel running on
+ * another stream meanwhile is not disturbed); each check reports what was
+ * added since the previous one, whichever stream it came from.
  */
 QUIK_API quik_status quik_sync_check(quik_stream_t stream);
 

@@ -23,6 +23,7 @@ HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "quik.h")
 
 QUIK_OK, QUIK_ERR_INVALID_ARG, QUIK_ERR_UNSUPPORTED, QUIK_ERR_CUDA, QUIK_ERR_TIMEOUT = range(5)
 QUIK_OUTLIER_FP16, QUIK_OUTLIER_INT8 = 0, 1
+QUIK_KV_FP16, QUIK_KV_INT8, QUIK_KV_INT4 = range(3)
 GROUP = 128
 
 
@@ -39,8 +40,29 @@ class quik_shape(ctypes.Structure):
                 ("weight_bits", ctypes.c_int32)]
 
 
+class quik_heads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("tokens", "q_heads", "kv_heads", "head_dim",
+                                              "rotary_dim", "interleaved", "table_rows")]
+
+
+class quik_kv_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("kv_type", "heads", "head_dim", "page_size", "pages",
+                                              "reserved")]
+    _fields_ += [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")]
+
+
+class quik_attention(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("tokens", "sequences", "q_heads", "max_tokens",
+                                              "max_pages", "max_context", "mask_words")]
+    _fields_ += [("scale", ctypes.c_float)]
+
+
 _P = ctypes.c_void_p
+_I64 = ctypes.c_int64
 _S = ctypes.POINTER(quik_shape)
+_H = ctypes.POINTER(quik_heads)
+_C = ctypes.POINTER(quik_kv_cache)
+_A = ctypes.POINTER(quik_attention)
 _SIGS = {
     "quik_workspace_size": (ctypes.c_size_t, [_S]),
     "quik_quantize_reorder": (ctypes.c_int, [_S, _P, _P, _P, _P, _P, _P, _P]),
@@ -61,6 +83,13 @@ _SIGS = {
     "quik_gemm_24_i32_debug": (ctypes.c_int, [_S] + [_P] * 8),
     "quik_expand_weights_24": (ctypes.c_int, [_S, _P, _P, _P, _P]),
     "quik_workspace_size_24": (ctypes.c_size_t, [_S]),
+    "quik_qk_norm_rope": (ctypes.c_int, [_H, _P, _I64, _P, _I64, _P, _P, ctypes.c_float, _P, _P, _P,
+                                         _P, _I64, _P, _I64, _P]),
+    "quik_kv_append": (ctypes.c_int, [_H, _C, _P, _I64, _P, _I64, _P, _P, _P, _P, _P]),
+    "quik_kv_gather": (ctypes.c_int, [_C, ctypes.c_int32, _P, _P, _I64, _P, _I64, _P]),
+    "quik_attention_workspace_size": (ctypes.c_size_t, [_A, _C]),
+    "quik_tree_attention": (ctypes.c_int, [_A, _C, _P, _I64, _P, _P, _P, _P, _P, _I64, _P, _P,
+                                           ctypes.c_size_t, _P]),
     "quik_sync_check": (ctypes.c_int, [_P]),
     "quik_selftest_timeout": (ctypes.c_int, [ctypes.c_uint32, _P]),
     "quik_test_stall": (ctypes.c_int, [ctypes.c_int]),
@@ -273,6 +302,118 @@ def quik_expand_weights_24(shape, Wq24, Wmeta, Wq, stream=None):
 
 def quik_workspace_size_24(shape: quik_shape) -> int:
     return int(lib().quik_workspace_size_24(ctypes.byref(shape)))
+
+
+def _rows(t, what, heads=None, dim=None):
+    """(pointer, row stride in elements) of fp16 rows [tokens, heads, head_dim]: the heads of a
+    token are contiguous, the tokens may be any distance apart (a slice of a projection's output)."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must live on a CUDA device")
+    if t.dtype != torch.float16:
+        raise TypeError(f"{what} must be torch.float16, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{what} must be [tokens, heads, head_dim], got {tuple(t.shape)}")
+    n, h, d = t.shape
+    if (heads is not None and h != heads) or (dim is not None and d != dim):
+        raise ValueError(f"{what} must have {heads} heads of {dim}, got {h} of {d}")
+    sn, sh, sd = t.stride()
+    if (sd != 1 and d > 1) or (sh != d and h > 1):
+        raise ValueError(f"{what}: the heads of a token must be contiguous")
+    if t.numel() == 0:
+        return None, h * d
+    return t.data_ptr(), sn if n > 1 else -(-h * d // 8) * 8
+
+
+def _same_device(*tensors):
+    """The one device of the tensors given."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError(f"tensors on {dev} and on {t.device}")
+    return dev
+
+
+class _on:
+    """Launch on the tensors' device and on `stream` (None: that device's current stream); what is
+    allocated inside belongs to that stream."""
+
+    def __init__(self, device, stream):
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream of {stream.device}, tensors on {device}")
+        self.contexts = []
+        if device.index is not None and device.index != torch.cuda.current_device():
+            self.contexts.append(torch.cuda.device(device))
+        if stream is not None:
+            self.contexts.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.contexts:
+            c.__enter__()
+
+    def __exit__(self, *exc):
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
+
+
+def _tables(cos, sin, positions, tokens):
+    """(rotary_dim, table rows) of the rotation's tables, or (0, 0) without them."""
+    if cos is None and sin is None:
+        return 0, 0
+    if cos is None or sin is None or positions is None:
+        raise ValueError("a rotation needs cos, sin and positions")
+    if cos.dim() != 2 or cos.shape != sin.shape:
+        raise ValueError("cos and sin must be [rows, rotary_dim / 2], both alike")
+    if positions.shape != (tokens,):
+        raise ValueError(f"positions must be [{tokens}], got {tuple(positions.shape)}")
+    return 2 * cos.shape[1], cos.shape[0]
+
+
+def quik_qk_norm_rope(heads, q, k, q_gamma, k_gamma, eps, cos, sin, positions, q_out, k_out,
+                      stream=None):
+    (qp, qs), (kp, ks) = _rows(q, "q"), _rows(k, "k")
+    (qo, qos), (ko, kos) = _rows(q_out, "q_out"), _rows(k_out, "k_out")
+    _check(lib().quik_qk_norm_rope(
+        ctypes.byref(heads), qp, qs, kp, ks, _ptr(q_gamma, torch.float16, "q_gamma"),
+        _ptr(k_gamma, torch.float16, "k_gamma"), float(eps), _ptr(cos, torch.float32, "cos"),
+        _ptr(sin, torch.float32, "sin"), _ptr(positions, torch.int32, "positions"), qo, qos, ko, kos,
+        _stream(stream)), "quik_qk_norm_rope")
+
+
+def quik_kv_append(heads, cache, k, v, cos, sin, positions, slots, stream=None):
+    (kp, ks), (vp, vs) = _rows(k, "k"), _rows(v, "v")
+    _check(lib().quik_kv_append(
+        ctypes.byref(heads), ctypes.byref(cache), kp, ks, vp, vs, _ptr(cos, torch.float32, "cos"),
+        _ptr(sin, torch.float32, "sin"), _ptr(positions, torch.int32, "positions"),
+        _ptr(slots, torch.int64, "slots"), _stream(stream)), "quik_kv_append")
+
+
+def quik_kv_gather(cache, slots, k_out, v_out, stream=None):
+    (kp, ks), (vp, vs) = _rows(k_out, "k_out"), _rows(v_out, "v_out")
+    _check(lib().quik_kv_gather(
+        ctypes.byref(cache), slots.numel(), _ptr(slots, torch.int64, "slots"), kp, ks, vp, vs,
+        _stream(stream)), "quik_kv_gather")
+
+
+def quik_attention_workspace_size(attention, cache) -> int:
+    return int(lib().quik_attention_workspace_size(ctypes.byref(attention), ctypes.byref(cache)))
+
+
+def quik_tree_attention(attention, cache, q, page_table, context, cu_tokens, tree_mask, out, lse,
+                        workspace, stream=None):
+    (qp, qs), (op, os_) = _rows(q, "q"), _rows(out, "out")
+    _check(lib().quik_tree_attention(
+        ctypes.byref(attention), ctypes.byref(cache), qp, qs,
+        _ptr(page_table, torch.int32, "page_table"), _ptr(context, torch.int32, "context"),
+        _ptr(cu_tokens, torch.int32, "cu_tokens"), _ptr(tree_mask, torch.int32, "tree_mask"), op, os_,
+        _ptr(lse, torch.float32, "lse"), _ptr(workspace, torch.uint8, "workspace"),
+        workspace.numel() if workspace is not None else 0, _stream(stream)), "quik_tree_attention")
 
 
 def quik_sync_check(stream=None) -> int:
@@ -502,3 +643,146 @@ class QuikLinear:
             quik_linear(self.shape(M), X, self.perm, self.Wq, self.w_scale, self.Wo, self.wo_scale,
                         self.bias, Y, self.workspace(M, X.device), stream=stream)
         return Y
+
+
+# ------------------------------------------------------------------ attention
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, q_weight=None, k_weight=None,
+                 eps: float = 1e-6, cos=None, sin=None, positions=None, interleaved: bool = False,
+                 q_out=None, k_out=None, stream=None):
+    """The RMS norm of each query and key head (weights fp16 [head_dim], None: no norm) and the
+    rotation by cos / sin fp32 [rows, rotary_dim / 2] at positions int32 [tokens] (None: none), in
+    one pass.  q [tokens, q_heads, head_dim] and k fp16, slices of a projection's rows as they are;
+    returns (q_out, k_out), new tensors unless given (each may be its input)."""
+    n, qh, d = q.shape
+    if k is not None and (k.shape[0] != n or k.shape[2] != d):
+        raise ValueError(f"k must be [{n}, heads, {d}], got {tuple(k.shape)}")
+    kh = 0 if k is None else k.shape[1]
+    rotary, rows = _tables(cos, sin, positions, n)
+    for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and w.shape != (d,):
+            raise ValueError(f"{what} must be [{d}], got {tuple(w.shape)}")
+    for o, x, what in ((q_out, q, "q_out"), (k_out, k, "k_out")):
+        if o is not None and (x is None or o.shape != x.shape):
+            raise ValueError(f"{what} must have its input's shape")
+    dev = _same_device(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out)
+    with _on(dev, stream):
+        if q_out is None:
+            q_out = torch.empty((n, qh, d), dtype=torch.float16, device=dev)
+        if k_out is None and k is not None:
+            k_out = torch.empty((n, kh, d), dtype=torch.float16, device=dev)
+        quik_qk_norm_rope(quik_heads(n, qh, kh, d, rotary, bool(interleaved), rows), q, k, q_weight,
+                          k_weight, eps, cos, sin, positions, q_out, k_out)
+    return q_out, k_out
+
+
+class QuikKVCache:
+    """A paged KV cache over the caller's buffers: k, v [pages, heads, page_size, row], fp16 with
+    row = head_dim, int8 (INT8 codes), or uint8 with row = head_dim / 2 (packed INT4); k_scale,
+    v_scale fp32 [pages, heads, page_size] for the quantised types."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale=None, v_scale=None):
+        kinds = {torch.float16: (QUIK_KV_FP16, 1), torch.int8: (QUIK_KV_INT8, 1),
+                 torch.uint8: (QUIK_KV_INT4, 2)}
+        if k.dtype not in kinds or k.dim() != 4:
+            raise TypeError(f"k must be fp16, int8 or uint8 [pages, heads, page_size, row], got {k.dtype} "
+                            f"{tuple(k.shape)}")
+        kind, per = kinds[k.dtype]
+        if v.shape != k.shape:
+            raise ValueError("v must have the shape of k")
+        pages, heads, page_size, row = k.shape
+        if (kind == QUIK_KV_FP16) != (k_scale is None) or (k_scale is None) != (v_scale is None):
+            raise ValueError("the quantised types, and only they, have k_scale and v_scale")
+        for s in (k_scale, v_scale):
+            if s is not None and s.shape != (pages, heads, page_size):
+                raise ValueError(f"scales must be [{pages}, {heads}, {page_size}], got {tuple(s.shape)}")
+        self.device = _same_device(k, v, k_scale, v_scale)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.heads, self.head_dim, self.page_size, self.pages = heads, row * per, page_size, pages
+        self.struct = quik_kv_cache(kind, heads, row * per, page_size, pages, 0, _ptr(k, k.dtype, "k"),
+                                    _ptr(v, k.dtype, "v"), _ptr(k_scale, torch.float32, "k_scale"),
+                                    _ptr(v_scale, torch.float32, "v_scale"))
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, head_dim: int, page_size: int = 64, bits: int = 16,
+              device="cuda") -> "QuikKVCache":
+        """A cache of zeros: 16-bit (fp16), 8-bit or 4-bit rows."""
+        if bits not in (16, 8, 4):
+            raise ValueError(f"bits must be 16, 8 or 4, got {bits}")
+        dtype, row = {16: (torch.float16, head_dim), 8: (torch.int8, head_dim),
+                      4: (torch.uint8, head_dim // 2)}[bits]
+        k, v = (torch.zeros((pages, heads, page_size, row), dtype=dtype, device=device) for _ in "kv")
+        ks = vs = None
+        if bits < 16:
+            ks, vs = (torch.zeros((pages, heads, page_size), dtype=torch.float32, device=device)
+                      for _ in "kv")
+        return cls(k, v, ks, vs)
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cos=None, sin=None,
+               positions=None, interleaved: bool = False, stream=None) -> None:
+        """quik_kv_append: rows k, v fp16 [tokens, heads, head_dim] into slots int64 [tokens]
+        (negative: left out), the keys rotated by cos / sin at positions on the way."""
+        n = k.shape[0]
+        if k.shape != (n, self.heads, self.head_dim) or v.shape != k.shape:
+            raise ValueError(f"k and v must be [tokens, {self.heads}, {self.head_dim}], got "
+                             f"{tuple(k.shape)} and {tuple(v.shape)}")
+        if slots.shape != (n,):
+            raise ValueError(f"slots must be [{n}], got {tuple(slots.shape)}")
+        rotary, rows = _tables(cos, sin, positions, n)
+        with _on(_same_device(self.k, k, v, slots, cos, sin, positions), stream):
+            quik_kv_append(quik_heads(n, 0, self.heads, self.head_dim, rotary, bool(interleaved), rows),
+                           self.struct, k, v, cos, sin, positions, slots)
+
+    def gather(self, slots: torch.Tensor, k_out=None, v_out=None, stream=None):
+        """quik_kv_gather: (k, v) fp16 [tokens, heads, head_dim] of slots int64 [tokens]."""
+        if slots.dim() != 1:
+            raise ValueError(f"slots must be [tokens], got {tuple(slots.shape)}")
+        shape = (slots.shape[0], self.heads, self.head_dim)
+        for o in (k_out, v_out):
+            if o is not None and o.shape != shape:
+                raise ValueError(f"outputs must be {shape}, got {tuple(o.shape)}")
+        with _on(_same_device(self.k, slots, k_out, v_out), stream):
+            if k_out is None:
+                k_out = torch.empty(shape, dtype=torch.float16, device=self.device)
+            if v_out is None:
+                v_out = torch.empty(shape, dtype=torch.float16, device=self.device)
+            quik_kv_gather(self.struct, slots, k_out, v_out)
+        return k_out, v_out
+
+
+def tree_attention(q: torch.Tensor, cache: QuikKVCache, page_table: torch.Tensor,
+                   context: torch.Tensor, cu_tokens: torch.Tensor, max_tokens: int, max_context: int,
+                   mask: torch.Tensor | None = None, scale: float | None = None, out=None, lse=None,
+                   return_lse: bool = False, stream=None):
+    """quik_tree_attention: attention of new tokens q fp16 [tokens, q_heads, head_dim] over the
+    cache.  page_table int32 [sequences, max_pages], context int32 [sequences], cu_tokens int32
+    [sequences + 1]; max_tokens and max_context are the largest number of new tokens and the largest
+    context of a sequence, known to the caller (nothing is read back from the device).  mask int32
+    [tokens, words]: bit j of a row, the new token j it sees (None: a chain).  scale defaults to
+    head_dim ** -0.5.  Returns out [tokens, q_heads, head_dim], with return_lse (out, lse fp32
+    [tokens, q_heads]).  Rows that belong to no sequence are left as they were (in new tensors:
+    undefined)."""
+    n, qh, d = q.shape
+    if d != cache.head_dim:
+        raise ValueError(f"q must have heads of {cache.head_dim}, got {d}")
+    B = context.numel()
+    if context.dim() != 1 or page_table.dim() != 2 or page_table.shape[0] != B or cu_tokens.shape != (B + 1,):
+        raise ValueError("context must be [sequences], page_table [sequences, max_pages], cu_tokens "
+                         "[sequences + 1]")
+    if mask is not None and (mask.dim() != 2 or mask.shape[0] != n):
+        raise ValueError(f"mask must be [{n}, words], got {tuple(mask.shape)}")
+    if out is not None and out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    if lse is not None and lse.shape != (n, qh):
+        raise ValueError(f"lse must be [{n}, {qh}], got {tuple(lse.shape)}")
+    a = quik_attention(n, B, qh, max_tokens, page_table.shape[1], max_context,
+                       0 if mask is None else mask.shape[1], d ** -0.5 if scale is None else scale)
+    dev = _same_device(cache.k, q, page_table, context, cu_tokens, mask, out, lse)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((n, qh, d), dtype=torch.float16, device=dev)
+        if lse is None and return_lse:
+            lse = torch.empty((n, qh), dtype=torch.float32, device=dev)
+        need = quik_attention_workspace_size(a, cache.struct)
+        ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+        quik_tree_attention(a, cache.struct, q, page_table, context, cu_tokens, mask, out, lse, ws)
+    return (out, lse) if return_lse else out

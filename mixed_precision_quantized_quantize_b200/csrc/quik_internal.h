@@ -77,7 +77,8 @@ cudaError_t launch_expand24(const uint8_t *Qs, const uint8_t *meta, int rows, in
 // resets them, so a kernel that compares the counter with the value it saw at
 // its start learns of every error recorded since.  A check reports the
 // increase since the previous check of the same counter on the current device.
-enum { kCounterGemmWaits = 0, kCounterQuantWaits = 1, kCounterBadPerm = 2, kCounterPGemmWaits = 3, kCounters = 4 };
+enum { kCounterGemmWaits = 0, kCounterQuantWaits = 1, kCounterBadPerm = 2, kCounterPGemmWaits = 3,
+       kCounterBadRow = 4, kCounterBadPage = 5, kCounters = 6 };
 unsigned counter_increase(int counter, unsigned value);
 // Expired waits in the quantise kernels since the last check (returned), and
 // perm entries outside [0, K) met since the last check (in *bad_perm when
@@ -133,6 +134,69 @@ cudaError_t set_persistent_gemm_stall(int on);
 bool make_map(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint64_t inner,
               uint64_t rows, uint64_t stride, uint32_t box_inner, uint32_t box_rows,
               CUtensorMapSwizzle sw);
+
+// ---------------------------------------------------------------- attention
+// The rotation: cos, sin [rows, rotary / 2] fp32, one position a token.
+struct RotaryArgs {
+    int rotary = 0;  // channels rotated (0: none)
+    int rows = 0;    // rows of the tables
+    bool interleaved = false;
+    const float *cos = nullptr, *sin = nullptr;
+    const int32_t *positions = nullptr;
+};
+
+// RMS norm of each head (gamma NULL: none) and rotation; strides in elements.
+struct QkArgs {
+    int tokens, q_heads, kv_heads, head_dim;
+    const uint16_t *q, *k;
+    int64_t q_stride, k_stride;
+    const uint16_t *q_gamma, *k_gamma;
+    float eps;
+    RotaryArgs rot;
+    uint16_t *q_out, *k_out;
+    int64_t q_out_stride, k_out_stride;
+};
+cudaError_t launch_qk_norm_rope(const QkArgs &a, cudaStream_t stream);
+
+struct AppendArgs {
+    int tokens;
+    quik_kv_cache cache;
+    const uint16_t *k, *v;
+    int64_t k_stride, v_stride;
+    RotaryArgs rot;
+    const int64_t *slots;
+};
+cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t stream);
+
+struct GatherArgs {
+    int tokens;
+    quik_kv_cache cache;
+    const int64_t *slots;
+    uint16_t *k_out, *v_out;
+    int64_t k_stride, v_stride;
+};
+cudaError_t launch_kv_gather(const GatherArgs &a, cudaStream_t stream);
+// Positions and slots out of range met by the row kernels since the last check.
+unsigned int take_row_errors();
+
+struct AttentionArgs {
+    int tokens, sequences, q_heads, max_tokens, max_pages, max_context, mask_words;
+    float scale;
+    quik_kv_cache cache;
+    const uint16_t *q;
+    int64_t q_stride;
+    const int32_t *page_table, *context, *cu_tokens;
+    const uint32_t *mask;  // NULL: a chain
+    uint16_t *out;
+    int64_t out_stride;
+    float *lse;  // optional
+    float *partial;  // split results (attention_workspace bytes), NULL when none is needed
+};
+size_t attention_workspace(const AttentionArgs &a);
+quik_status launch_tree_attention(const AttentionArgs &a, cudaStream_t stream);
+// Page numbers, lengths and offsets out of range met by the attention kernel
+// since the last check.
+unsigned int take_attention_errors();
 
 quik_status sync_check(cudaStream_t stream);
 quik_status launch_timeout_selftest(uint32_t limit_us, cudaStream_t stream);

@@ -1,0 +1,772 @@
+// tree_attention.cu -- attention of drafted tokens over the paged KV cache
+// (fp16, INT8 or packed INT4 rows).
+//
+// Per sequence and key head, the G = q_heads / heads query heads of the new
+// tokens are the rows of one small matrix (row r: new token r / G, head r % G),
+// so that a cached row is read once for all of them.  For tiles of 32 cached
+// tokens:
+//     S = Q K^T             m16n8k16 products, fp32 sums
+//     t = scale * log2(e) * k_scale * S
+//     m' = max(m, max t), p = 2^(t - m' + 14), l += p, O = O 2^(m - m') + p V
+// The running maximum and sum are fp32.  p is rounded to fp16 for its product
+// with V; the factor 2^14 (it cancels in O / l) keeps p's far below the maximum
+// out of fp16's subnormal range, and p <= 2^14 stays below its largest value.
+// Quantised values enter the product as their integer codes, exact in fp16;
+// their scale multiplies p in fp32 before that rounding, relative to a running
+// power of two 2^R above every scale met so far (O then is in units of 2^R), so
+// p stays within fp16 whatever the scales are.
+#include "quik_internal.h"
+
+#include <cuda_fp16.h>
+
+namespace quik {
+
+// Indices out of range met by the kernel (page numbers, lengths, offsets):
+// only ever grows; quik_sync_check reports the increase.
+__device__ unsigned int g_attn_bad_index;
+
+namespace {
+
+constexpr int kTile = 32;          // cached tokens per tile
+constexpr float kShift = 14.0f;    // p carries 2^14
+constexpr int kMaxSplits = 64;
+
+struct Params {
+    int tokens, sequences, q_heads, heads, group, max_tokens, max_pages, mask_words;
+    int pages, page_shift, splits, row_blocks;
+    float scale_log2;
+    const uint16_t *q;
+    int64_t q_stride;
+    const uint8_t *k, *v;
+    const float *ks, *vs;
+    const int32_t *page_table, *context, *cu;
+    const uint32_t *mask;
+    uint16_t *out;
+    int64_t out_stride;
+    float *lse;
+    float *part_o;   // [splits][tokens * q_heads][D]
+    float2 *part_ml; // [splits][tokens * q_heads]
+};
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// 16 (or 4) bytes global -> shared, zeros where !ok (nothing is read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void group_sync(int id, int threads) {
+    if (threads == 32)
+        __syncwarp();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pick(uint32_t a, uint32_t b, uint32_t sel) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+    return r;
+}
+__device__ __forceinline__ uint32_t half2_sub(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void load_matrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void load_matrix4_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+template <int BYTES>
+__device__ __forceinline__ void load_words(uint32_t (&w)[BYTES / 4], uint32_t addr) {
+    if constexpr (BYTES == 16)
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(addr)
+                     : "memory");
+    else if constexpr (BYTES == 8)
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+    else
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
+}
+
+// Codes to fp16, exactly: a code's bits (offset to be non-negative) are put
+// into the mantissa of 2^10 (or, four bits up, of 2^6), and that base plus the
+// offset is subtracted.
+constexpr uint32_t kBase8 = 0x64006400u;    // 1024, 1024
+constexpr uint32_t kSub8 = 0x64806480u;     // 1024 + 128
+constexpr uint32_t kBase4 = 0x64006400u;    // 1024: nibble in bits 0-3
+constexpr uint32_t kSub4 = 0x64086408u;     // 1024 + 8
+constexpr uint32_t kBase4Up = 0x54005400u;  // 64: nibble in bits 4-7
+constexpr uint32_t kSub4Up = 0x54805480u;   // 64 + 8
+// bytes 0, 1 (hi: 2, 3) of x (already ^ 0x80) as a pair
+__device__ __forceinline__ uint32_t pair8(uint32_t x, bool hi) {
+    return half2_sub(pick(x, kBase8, hi ? 0x5352u : 0x5150u), kSub8);
+}
+// the nibbles at bits 0 and 16 (up: 4 and 20) of x (already ^ 8) as a pair
+__device__ __forceinline__ uint32_t pair4(uint32_t x, bool up) {
+    return up ? half2_sub((x & 0x00f000f0u) | kBase4Up, kSub4Up)
+              : half2_sub((x & 0x000f000fu) | kBase4, kSub4);
+}
+
+// WR warps share a tile, 16 rows each; NW / WR such groups take tiles in turn.
+template <int BITS_, int D_, int WR_, int NW_>
+struct Cfg {
+    static constexpr int BITS = BITS_, D = D_, WR = WR_, NW = NW_;
+    static constexpr int TG = NW / WR;
+    static constexpr int RB = D * BITS / 8;  // bytes of a cached row
+    static constexpr int CPR = RB / 16;
+    // row pitches in shared memory: with 16 bytes of padding the 8 rows that a
+    // fragment load touches fall into different banks; rows of 32 or 64 bytes
+    // of K are read whole, in order, and need none
+    static constexpr int KS = RB >= 128 ? RB + 16 : RB;
+    static constexpr int VS = RB + 16;
+    static constexpr int SCALES = BITS == 16 ? 0 : 2 * kTile * 4;
+    static constexpr int STAGE = kTile * (KS + VS) + SCALES + 16;
+    static constexpr int STAGES = 3;
+    static constexpr int RING = TG * STAGES * STAGE;
+    static constexpr int OP = D + 4;  // pitch of an output row at the merge (floats)
+    static constexpr int MERGE = NW * 16 * OP * 4 + NW * 16 * 8;
+    static constexpr int SMEM = RING > MERGE ? RING : MERGE;
+    static constexpr int ROWS = 16 * WR;
+    static constexpr int STEPS = D / 16;  // products along a head
+    static constexpr int NT = D / 8;      // output column tiles
+};
+
+// What a sequence holds; n == 0: nothing to do.
+struct Seq {
+    int first, n, ctx, total;
+};
+__device__ __forceinline__ Seq sequence(const Params &p, int b, bool report) {
+    Seq s;
+    s.first = p.cu[b];
+    const int end = p.cu[b + 1];
+    s.ctx = p.context[b];
+    const int64_t cap = min(static_cast<int64_t>(p.max_pages) << p.page_shift,
+                            static_cast<int64_t>(0x7fffff00));
+    int64_t total = static_cast<int64_t>(s.ctx) + (static_cast<int64_t>(end) - s.first);
+    bool bad = s.first < 0 || end < s.first || end > p.tokens || s.ctx < 0;
+    if (!bad) bad = end - s.first > p.max_tokens;
+    s.n = bad ? 0 : end - s.first;
+    if (!bad && total > cap) {
+        total = cap;
+        if (report) atomicAdd(&g_attn_bad_index, 1u);
+    }
+    if (bad && report) atomicAdd(&g_attn_bad_index, 1u);
+    s.total = bad ? 0 : static_cast<int>(total);
+    return s;
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::NW * 32) tree_attention_kernel(const Params p) {
+    constexpr int BITS = C::BITS, D = C::D, WR = C::WR, TG = C::TG;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int tg = warp / WR, wr = warp % WR;
+    const int split = blockIdx.x % p.splits, rb = blockIdx.x / p.splits;
+    const int h = blockIdx.y, b = blockIdx.z;
+    const Seq sq = sequence(p, b, blockIdx.x == 0 && h == 0 && threadIdx.x == 0);
+    const int rows = sq.n * p.group;
+    if (rb * C::ROWS >= rows) return;
+
+    // this split's tiles
+    const int tiles = (sq.total + kTile - 1) / kTile;
+    const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * split / p.splits);
+    const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / p.splits);
+
+    // ---- the query rows of this lane, as the products' first operand
+    const int q4 = lane & 3, q8 = lane >> 2;
+    int tok[2];  // new token of rows q8 and q8 + 8 of this warp, -1: no such row
+    uint32_t qf[C::STEPS][4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int r = rb * C::ROWS + wr * 16 + q8 + 8 * e;
+        tok[e] = r < rows ? r / p.group : -1;
+        const uint16_t *src = p.q;
+        if (tok[e] >= 0)
+            src += static_cast<int64_t>(sq.first + tok[e]) * p.q_stride +
+                   static_cast<int64_t>(h * p.group + r % p.group) * D;
+        if constexpr (BITS == 16) {
+#pragma unroll
+            for (int s = 0; s < C::STEPS; ++s)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    qf[s][e + 2 * x] =
+                        tok[e] >= 0 ? *reinterpret_cast<const uint32_t *>(src + 16 * s + 8 * x + 2 * q4) : 0u;
+        } else {
+            // a lane's K operand is D / 4 consecutive channels; the order in
+            // which its words give them up is the order of q here
+            uint32_t w[D / 8];
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (tok[e] >= 0) u = *reinterpret_cast<const uint4 *>(src + q4 * (D / 4) + 8 * i);
+                w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+            }
+#pragma unroll
+            for (int s = 0; s < C::STEPS; ++s) {
+                if constexpr (BITS == 8) {
+                    qf[s][e] = w[2 * s], qf[s][e + 2] = w[2 * s + 1];
+                } else {
+                    // eight codes of a word: pairs (0, 4), (1, 5), then (2, 6), (3, 7)
+                    const uint32_t lo = w[4 * (s / 2) + s % 2], hi = w[4 * (s / 2) + 2 + s % 2];
+                    qf[s][e] = pick(lo, hi, 0x5410u), qf[s][e + 2] = pick(lo, hi, 0x7632u);
+                }
+            }
+        }
+    }
+
+    // ---- copies of a tile
+    uint8_t *ring = smem + tg * C::STAGES * C::STAGE;
+    const int32_t *table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
+    const int page_mask = (1 << p.page_shift) - 1;
+    auto page_of = [&](int tile) -> int {  // of token `lane` of the tile; -1: none
+        const int pos = tile * kTile + lane;
+        if (tile >= t1 || pos >= sq.total) return -1;
+        const int id = table[pos >> p.page_shift];
+        if (id >= 0 && id < p.pages) return id;
+        if (wr == 0 && rb == 0) atomicAdd(&g_attn_bad_index, 1u);
+        return -1;
+    };
+    auto issue = [&](int tile, int stage, int id) {
+        uint8_t *st = ring + stage * C::STAGE;
+        const uint32_t ka = smem_addr(st), va = ka + kTile * C::KS;
+        const unsigned live = __ballot_sync(0xffffffffu, id >= 0);
+        constexpr int TH = 32 * WR;
+        const int gt = wr * 32 + lane;
+#pragma unroll
+        for (int i = 0; i < (kTile * C::CPR + TH - 1) / TH; ++i) {
+            const int x = i * TH + gt, t = x / C::CPR, c = x % C::CPR;
+            const int pid = __shfl_sync(0xffffffffu, id, t & 31);
+            const bool ok = pid >= 0;
+            const int64_t row = ((static_cast<int64_t>(ok ? pid : 0) * p.heads + h) << p.page_shift) +
+                                ((tile * kTile + t) & page_mask);
+            const int64_t off = ok ? row * C::RB + c * 16 : 0;
+            if (kTile * C::CPR % TH == 0 || x < kTile * C::CPR) {
+                copy16(ka + t * C::KS + c * 16, p.k + off, ok);
+                copy16(va + t * C::VS + c * 16, p.v + off, ok);
+            }
+        }
+        uint8_t *tail = st + kTile * (C::KS + C::VS);
+        if (wr == 0) {
+            if constexpr (BITS != 16) {
+                const bool ok = id >= 0;
+                const int64_t row = ((static_cast<int64_t>(ok ? id : 0) * p.heads + h) << p.page_shift) +
+                                    ((tile * kTile + lane) & page_mask);
+                copy4(smem_addr(tail) + 4 * lane, p.ks + (ok ? row : 0), ok);
+                copy4(smem_addr(tail) + 4 * (kTile + lane), p.vs + (ok ? row : 0), ok);
+            }
+            if (lane == 0) *reinterpret_cast<unsigned *>(tail + C::SCALES) = live;
+        }
+    };
+
+    float o[C::NT][4];
+#pragma unroll
+    for (int i = 0; i < C::NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    int R = -100;  // exponent of the unit of o (quantised values)
+
+    int next = t0 + tg;  // tile to be issued next, and its pages
+    int id = page_of(next);
+#pragma unroll
+    for (int s = 0; s < C::STAGES - 1; ++s) {
+        if (next < t1) issue(next, s, id);
+        copy_commit();
+        next += TG;
+        id = page_of(next);
+    }
+
+    int stage = 0;
+    for (int t = t0 + tg; t < t1; t += TG) {
+        copy_wait<C::STAGES - 2>();
+        group_sync(1 + tg, 32 * WR);
+        {
+            int free_stage = stage + C::STAGES - 1;
+            if (free_stage >= C::STAGES) free_stage -= C::STAGES;
+            if (next < t1) issue(next, free_stage, id);
+            copy_commit();
+            next += TG;
+            id = page_of(next);
+        }
+        const uint8_t *st = ring + stage * C::STAGE;
+        const uint32_t ka = smem_addr(st), va = ka + kTile * C::KS;
+        const uint8_t *tail = st + kTile * (C::KS + C::VS);
+        if (++stage == C::STAGES) stage = 0;
+
+        // ---- S = Q K^T: column 8 n + 2 q4 + e is token 8 n + 2 q4 + e of the tile
+        float s[4][4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[n][j] = 0.0f;
+            if constexpr (BITS == 16) {
+#pragma unroll
+                for (int k = 0; k < C::STEPS / 2; ++k) {
+                    uint32_t f[4];
+                    load_matrix4(f, ka + (8 * n + (lane & 7)) * C::KS + (4 * k + (lane >> 3)) * 16);
+                    mma(s[n], qf[2 * k], f[0], f[1]);
+                    mma(s[n], qf[2 * k + 1], f[2], f[3]);
+                }
+            } else {
+                constexpr int LB = C::RB / 4, UB = LB < 16 ? LB : 16;
+                const uint32_t at = ka + (8 * n + q8) * C::KS + q4 * LB;
+#pragma unroll
+                for (int u = 0; u < LB / UB; ++u) {
+                    uint32_t w[UB / 4];
+                    load_words<UB>(w, at + u * UB);
+#pragma unroll
+                    for (int i = 0; i < UB / 4; ++i) {
+                        if constexpr (BITS == 8) {
+                            const uint32_t x = w[i] ^ 0x80808080u;
+                            mma(s[n], qf[u * (UB / 4) + i], pair8(x, false), pair8(x, true));
+                        } else {
+                            const uint32_t x = w[i] ^ 0x88888888u, y = x >> 8;
+                            const int k = 2 * (u * (UB / 4) + i);
+                            mma(s[n], qf[k], pair4(x, false), pair4(x, true));
+                            mma(s[n], qf[k + 1], pair4(y, false), pair4(y, true));
+                        }
+                    }
+                }
+            }
+        }
+        // ---- scores in log2 units, unseen ones -infinity
+        float vsc[4][2];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            float2 ksc = make_float2(1.0f, 1.0f);
+            if constexpr (BITS != 16) {
+                ksc = *reinterpret_cast<const float2 *>(tail + 4 * (8 * n + 2 * q4));
+                const float2 v2 = *reinterpret_cast<const float2 *>(tail + 4 * (kTile + 8 * n + 2 * q4));
+                vsc[n][0] = v2.x, vsc[n][1] = v2.y;
+            }
+            const float a = ksc.x * p.scale_log2, c = ksc.y * p.scale_log2;
+            s[n][0] *= a, s[n][1] *= c, s[n][2] *= a, s[n][3] *= c;
+        }
+        const unsigned live = *reinterpret_cast<const unsigned *>(tail + C::SCALES);
+        const int j0 = t * kTile - sq.ctx;  // new token at the tile's first position
+        unsigned see[2] = {live, live};
+        const bool masked = live != 0xffffffffu || j0 + kTile > 0;
+        if (masked) {
+            if (j0 + kTile > 0) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    unsigned bits = 0;
+                    if (tok[e] < 0) {
+                        bits = 0xffffffffu;
+                    } else if (p.mask == nullptr) {
+                        const int top = tok[e] - j0;  // last visible position of the tile
+                        bits = top < 0 ? 0u : top >= 31 ? 0xffffffffu : (2u << top) - 1u;
+                    } else {
+                        const uint32_t *row =
+                            p.mask + static_cast<int64_t>(sq.first + tok[e]) * p.mask_words;
+                        if (j0 < 0) {
+                            bits = (row[0] << -j0) | ((1u << -j0) - 1u);
+                        } else {
+                            const int w = j0 / 32, sh = j0 % 32;
+                            const uint32_t lo = w < p.mask_words ? row[w] : 0u;
+                            const uint32_t hi = w + 1 < p.mask_words ? row[w + 1] : 0u;
+                            bits = __funnelshift_r(lo, hi, sh);
+                        }
+                    }
+                    see[e] &= bits;
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (!((see[j >> 1] >> (8 * n + 2 * q4 + (j & 1))) & 1u)) s[n][j] = -INFINITY;
+        }
+        // ---- running maximum
+        float alpha[2], base[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float x = m[e];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) x = fmaxf(x, fmaxf(s[n][2 * e], s[n][2 * e + 1]));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+            base[e] = x == -INFINITY ? 0.0f : x;
+            alpha[e] = exp2_fast(m[e] - base[e]);
+            m[e] = x;
+            l[e] *= alpha[e];
+            base[e] -= kShift;
+        }
+        // ---- the unit of the values' scales
+        float unit = 1.0f;
+        if constexpr (BITS != 16) {
+            unsigned top = 0;  // largest finite magnitude, by its bits
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const unsigned u = __float_as_uint(vsc[n][e]) & 0x7fffffffu;
+                    top = max(top, u < 0x7f800000u ? u : 0u);
+                }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int e = min(max(static_cast<int>(top >> 23) - 126, -100), 126);
+            if (e > R) {
+                const float f = exp2_fast(static_cast<float>(R - e));
+                alpha[0] *= f, alpha[1] *= f;
+                R = e;
+            }
+            unit = __uint_as_float(static_cast<unsigned>(127 - R) << 23);
+        }
+        if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
+#pragma unroll
+            for (int i = 0; i < C::NT; ++i) {
+                o[i][0] *= alpha[0], o[i][1] *= alpha[0];
+                o[i][2] *= alpha[1], o[i][3] *= alpha[1];
+            }
+        }
+        // ---- p
+        uint32_t pf[2][4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            float x[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[j] = exp2_fast(s[n][j] - base[j >> 1]);
+                l[j >> 1] += x[j];
+            }
+            if constexpr (BITS != 16) {
+                const float a = vsc[n][0] * unit, c = vsc[n][1] * unit;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] *= j & 1 ? c : a;
+                if (masked) {  // an unseen token's scale may be anything
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (!((see[j >> 1] >> (8 * n + 2 * q4 + (j & 1))) & 1u)) x[j] = 0.0f;
+                }
+            }
+            pf[n / 2][2 * (n % 2)] = half2_of(x[0], x[1]);
+            pf[n / 2][2 * (n % 2) + 1] = half2_of(x[2], x[3]);
+        }
+        // ---- O += P V
+        if constexpr (BITS == 16) {
+            // stored infinities and NaN in a tile that some row does not see
+            // whole: 0 * infinity would reach that row through the product
+            unsigned odd = 0;
+            if (masked) {
+                bool any = false;
+#pragma unroll
+                for (int c = 0; c < C::CPR; ++c) {
+                    uint32_t w[4];
+                    load_words<16>(w, va + lane * C::VS + 16 * c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        any |= (w[i] & 0x7c00u) == 0x7c00u || (w[i] & 0x7c000000u) == 0x7c000000u;
+                }
+                odd = __ballot_sync(0xffffffffu, any);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const unsigned o2 = odd >> (16 * k + 2 * q4);
+                const uint32_t keep0 = ~((o2 & 1u ? 0xffffu : 0u) | (o2 & 2u ? 0xffff0000u : 0u));
+                const uint32_t keep1 = ~((o2 & 256u ? 0xffffu : 0u) | (o2 & 512u ? 0xffff0000u : 0u));
+#pragma unroll
+                for (int i = 0; i < C::NT; i += 2) {
+                    uint32_t f[4];
+                    load_matrix4_t(f, va + (16 * k + (lane & 15)) * C::VS + (i + (lane >> 4)) * 16);
+                    if (odd != 0) f[0] &= keep0, f[1] &= keep1, f[2] &= keep0, f[3] &= keep1;
+                    mma(o[i], pf[k], f[0], f[1]);
+                    mma(o[i + 1], pf[k], f[2], f[3]);
+                }
+            }
+            // the tokens left out above, one by one, for the rows that see them
+            while (odd != 0) {
+                const int x = __ffs(odd) - 1;
+                odd &= odd - 1;
+                float pr[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mine = 0.0f;
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            if (8 * n + 2 * q4 + j == x) {
+                                const uint32_t w = pf[n / 2][2 * (n % 2) + e];
+                                const __half2 h2 = *reinterpret_cast<const __half2 *>(&w);
+                                mine = j ? __high2float(h2) : __low2float(h2);
+                            }
+                    pr[e] = __shfl_sync(0xffffffffu, mine, (lane & ~3) | ((x % 8) / 2));
+                }
+#pragma unroll
+                for (int i = 0; i < C::NT; ++i) {
+                    const uint32_t w = *reinterpret_cast<const uint32_t *>(
+                        st + kTile * C::KS + x * C::VS + (8 * i + 2 * q4) * 2);
+                    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+                    if ((see[0] >> x) & 1u) o[i][0] = fmaf(pr[0], v.x, o[i][0]), o[i][1] = fmaf(pr[0], v.y, o[i][1]);
+                    if ((see[1] >> x) & 1u) o[i][2] = fmaf(pr[1], v.x, o[i][2]), o[i][3] = fmaf(pr[1], v.y, o[i][3]);
+                }
+            }
+        } else {
+            // a lane's V operand is D / 8 consecutive channels of four tokens
+            // (column i of output tile c is channel c D / 8 + i)
+            constexpr int LB = C::RB / 8;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t w[4][LB / 4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    load_words<LB>(w[x], va + (16 * k + 2 * q4 + (x & 1) + 8 * (x >> 1)) * C::VS + q8 * LB);
+#pragma unroll
+                for (int i = 0; i < LB / 4; ++i) {
+                    if constexpr (BITS == 8) {
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const uint32_t sel = y ? 0x7362u : 0x5140u;
+                            const uint32_t a = pick(w[0][i], w[1][i], sel) ^ 0x80808080u;
+                            const uint32_t c = pick(w[2][i], w[3][i], sel) ^ 0x80808080u;
+                            mma(o[4 * i + 2 * y], pf[k], pair8(a, false), pair8(c, false));
+                            mma(o[4 * i + 2 * y + 1], pf[k], pair8(a, true), pair8(c, true));
+                        }
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const uint32_t sel = y ? 0x7632u : 0x5410u;
+                            const uint32_t a = pick(w[0][i], w[1][i], sel) ^ 0x88888888u, a2 = a >> 8;
+                            const uint32_t c = pick(w[2][i], w[3][i], sel) ^ 0x88888888u, c2 = c >> 8;
+                            mma(o[8 * i + 4 * y], pf[k], pair4(a, false), pair4(c, false));
+                            mma(o[8 * i + 4 * y + 1], pf[k], pair4(a, true), pair4(c, true));
+                            mma(o[8 * i + 4 * y + 2], pf[k], pair4(a2, false), pair4(c2, false));
+                            mma(o[8 * i + 4 * y + 3], pf[k], pair4(a2, true), pair4(c2, true));
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    // ---- join the warp groups' results in shared memory (the ring is done with)
+    copy_wait<0>();
+    __syncthreads();
+    float *mo = reinterpret_cast<float *>(smem) + warp * 16 * C::OP;
+    float2 *ml = reinterpret_cast<float2 *>(smem + C::NW * 16 * C::OP * 4);
+    const float up = BITS == 16 ? 1.0f : __uint_as_float(static_cast<unsigned>(127 + R) << 23);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+        if (q4 == 0) ml[warp * 16 + q8 + 8 * e] = make_float2(m[e], l[e]);
+#pragma unroll
+        for (int i = 0; i < C::NT; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int d = BITS == 16 ? 8 * i + 2 * q4 + j : (2 * q4 + j) * (D / 8) + i;
+                mo[(q8 + 8 * e) * C::OP + d] = o[i][2 * e + j] * up;
+            }
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < C::ROWS * (D / 4); x += C::NW * 32) {
+        const int r = x / (D / 4), d = x % (D / 4) * 4;
+        const int g = rb * C::ROWS + r;
+        if (g >= rows) break;
+        float M = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < TG; ++k) M = fmaxf(M, ml[(k * WR + r / 16) * 16 + r % 16].x);
+        const float base = M == -INFINITY ? 0.0f : M;
+        float L = 0.0f;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < TG; ++k) {
+            const int w = k * WR + r / 16;
+            const float2 a = ml[w * 16 + r % 16];
+            const float f = exp2_fast(a.x - base);
+            const float4 v = *reinterpret_cast<const float4 *>(
+                reinterpret_cast<const float *>(smem) + (w * 16 + r % 16) * C::OP + d);
+            L = fmaf(f, a.y, L);
+            acc.x = fmaf(f, v.x, acc.x), acc.y = fmaf(f, v.y, acc.y);
+            acc.z = fmaf(f, v.z, acc.z), acc.w = fmaf(f, v.w, acc.w);
+        }
+        const int head = h * p.group + g % p.group, token = sq.first + g / p.group;
+        const int64_t row = static_cast<int64_t>(token) * p.q_heads + head;
+        if (p.splits == 1) {
+            const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+            *reinterpret_cast<uint2 *>(p.out + static_cast<int64_t>(token) * p.out_stride + head * D + d) =
+                make_uint2(half2_of(acc.x * inv, acc.y * inv), half2_of(acc.z * inv, acc.w * inv));
+            if (d == 0 && p.lse != nullptr)
+                p.lse[row] = L == 0.0f ? -INFINITY : (M - kShift + log2f(L)) * 0.693147180559945f;
+        } else {
+            const int64_t at = static_cast<int64_t>(split) * p.tokens * p.q_heads + row;
+            *reinterpret_cast<float4 *>(p.part_o + at * D + d) = acc;
+            if (d == 0) p.part_ml[at] = make_float2(M, L);
+        }
+    }
+}
+
+// Join the splits' results: one warp a row.
+template <int D>
+__global__ void __launch_bounds__(128) tree_attention_join_kernel(const Params p) {
+    const int lane = threadIdx.x % 32;
+    const int h = blockIdx.y, b = blockIdx.z;
+    const Seq sq = sequence(p, b, false);
+    const int g = blockIdx.x * 4 + threadIdx.x / 32;
+    if (g >= sq.n * p.group) return;
+    const int head = h * p.group + g % p.group, token = sq.first + g / p.group;
+    const int64_t row = static_cast<int64_t>(token) * p.q_heads + head;
+    const int64_t step = static_cast<int64_t>(p.tokens) * p.q_heads;
+    float M = -INFINITY;
+    for (int s = lane; s < p.splits; s += 32) M = fmaxf(M, p.part_ml[s * step + row].x);
+#pragma unroll
+    for (int x = 1; x < 32; x *= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    const float base = M == -INFINITY ? 0.0f : M;
+    constexpr int V = D / 32;
+    float L = 0.0f, acc[V] = {};
+    for (int s = 0; s < p.splits; ++s) {
+        const float2 a = p.part_ml[s * step + row];
+        const float f = exp2_fast(a.x - base);
+        L = fmaf(f, a.y, L);
+        const float *src = p.part_o + (s * step + row) * D + lane * V;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = fmaf(f, src[i], acc[i]);
+    }
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    uint16_t *dst = p.out + static_cast<int64_t>(token) * p.out_stride + head * D + lane * V;
+#pragma unroll
+    for (int i = 0; i < V; i += 2)
+        *reinterpret_cast<uint32_t *>(dst + i) = half2_of(acc[i] * inv, acc[i + 1] * inv);
+    if (lane == 0 && p.lse != nullptr)
+        p.lse[row] = L == 0.0f ? -INFINITY : (M - kShift + log2f(L)) * 0.693147180559945f;
+}
+
+// ------------------------------------------------------------------ host side
+struct Plan {
+    int wr, row_blocks, splits;
+};
+
+// Row warps: the fewest that hold the rows (a warp's products have 16), up to
+// four.  Splits of the cached tokens: enough CTAs for about two a resident
+// slot, while each warp group keeps at least four tiles.
+Plan plan_of(const AttentionArgs &a) {
+    Plan r;
+    const int64_t rows = static_cast<int64_t>(a.max_tokens) * (a.q_heads / a.cache.heads);
+    r.wr = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+    r.row_blocks = static_cast<int>((rows + 16 * r.wr - 1) / (16 * r.wr));
+    const int64_t items = static_cast<int64_t>(a.sequences) * a.cache.heads * r.row_blocks;
+    const int64_t slots = static_cast<int64_t>(sm_count()) * 2;
+    const int64_t tiles = (static_cast<int64_t>(a.max_context) + a.max_tokens + kTile - 1) / kTile;
+    int64_t s = (2 * slots + items - 1) / items;
+    const int64_t most = tiles / (4 * (4 / r.wr));
+    s = s < most ? s : most;
+    s = s < kMaxSplits ? s : kMaxSplits;
+    r.splits = s < 1 ? 1 : static_cast<int>(s);
+    return r;
+}
+
+size_t partial_bytes(const AttentionArgs &a, int splits) {
+    if (splits == 1) return 0;
+    return static_cast<size_t>(splits) * a.tokens * a.q_heads * (a.cache.head_dim * 4 + 8);
+}
+
+template <class C>
+quik_status run(const Params &p, cudaStream_t stream) {
+    if (!attribute_set_once(reinterpret_cast<const void *>(&tree_attention_kernel<C>), C::SMEM))
+        return QUIK_ERR_CUDA;
+    const dim3 grid(p.splits * p.row_blocks, p.heads, p.sequences);
+    tree_attention_kernel<C><<<grid, C::NW * 32, C::SMEM, stream>>>(p);
+    if (p.splits > 1) {
+        const int64_t rows = static_cast<int64_t>(p.max_tokens) * p.group;
+        tree_attention_join_kernel<C::D>
+            <<<dim3(static_cast<unsigned>((rows + 3) / 4), p.heads, p.sequences), 128, 0, stream>>>(p);
+    }
+    return cudaGetLastError() == cudaSuccess ? QUIK_OK : QUIK_ERR_CUDA;
+}
+
+template <int BITS, int D>
+quik_status run_rows(const Params &p, int wr, cudaStream_t stream) {
+    if (wr == 1) return run<Cfg<BITS, D, 1, 4>>(p, stream);
+    if (wr == 2) return run<Cfg<BITS, D, 2, 4>>(p, stream);
+    return run<Cfg<BITS, D, 4, 4>>(p, stream);
+}
+
+template <int BITS>
+quik_status run_dim(const Params &p, int head_dim, int wr, cudaStream_t stream) {
+    return head_dim == 64 ? run_rows<BITS, 64>(p, wr, stream) : run_rows<BITS, 128>(p, wr, stream);
+}
+
+}  // namespace
+
+size_t attention_workspace(const AttentionArgs &a) { return partial_bytes(a, plan_of(a).splits); }
+
+quik_status launch_tree_attention(const AttentionArgs &a, cudaStream_t stream) {
+    const Plan plan = plan_of(a);
+    Params p;
+    p.tokens = a.tokens;
+    p.sequences = a.sequences;
+    p.q_heads = a.q_heads;
+    p.heads = a.cache.heads;
+    p.group = a.q_heads / a.cache.heads;
+    p.max_tokens = a.max_tokens;
+    p.max_pages = a.max_pages;
+    p.mask_words = a.mask_words;
+    p.pages = a.cache.pages;
+    p.page_shift = 0;
+    while ((1 << p.page_shift) < a.cache.page_size) ++p.page_shift;
+    p.splits = plan.splits;
+    p.row_blocks = plan.row_blocks;
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.q = a.q;
+    p.q_stride = a.q_stride;
+    p.k = static_cast<const uint8_t *>(a.cache.k);
+    p.v = static_cast<const uint8_t *>(a.cache.v);
+    p.ks = a.cache.k_scale;
+    p.vs = a.cache.v_scale;
+    p.page_table = a.page_table;
+    p.context = a.context;
+    p.cu = a.cu_tokens;
+    p.mask = a.mask;
+    p.out = a.out;
+    p.out_stride = a.out_stride;
+    p.lse = a.lse;
+    p.part_o = a.partial;
+    p.part_ml = reinterpret_cast<float2 *>(
+        a.partial + static_cast<size_t>(plan.splits) * a.tokens * a.q_heads * a.cache.head_dim);
+    if (a.cache.kv_type == QUIK_KV_INT4) return run_dim<4>(p, a.cache.head_dim, plan.wr, stream);
+    if (a.cache.kv_type == QUIK_KV_INT8) return run_dim<8>(p, a.cache.head_dim, plan.wr, stream);
+    return run_dim<16>(p, a.cache.head_dim, plan.wr, stream);
+}
+
+unsigned int take_attention_errors() {
+    unsigned int word = 0;
+    if (cudaMemcpyFromSymbol(&word, g_attn_bad_index, sizeof(word)) != cudaSuccess) return 0;
+    return counter_increase(kCounterBadPage, word);
+}
+
+}  // namespace quik
