@@ -304,52 +304,76 @@ def quik_workspace_size_24(shape: quik_shape) -> int:
     return int(lib().quik_workspace_size_24(ctypes.byref(shape)))
 
 
-def _rows(t, what, heads=None, dim=None):
-    """(pointer, row stride in elements) of fp16 rows [tokens, heads, head_dim]: the heads of a
-    token are contiguous, the tokens may be any distance apart (a slice of a projection's output)."""
-    if t is None:
-        return None, 0
+# The attention operators' calls take a few microseconds on the GPU, so what the
+# host does for each counts: a tensor's type and device are looked at once (a
+# device index of -1 is the CPU), the stream is read as a raw handle, and the C
+# function is called with plain integers.
+_F16, _F32, _I32, _L64 = torch.float16, torch.float32, torch.int32, torch.int64
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _refuse(t, what, dtype, dev):
+    """Say what is wrong with a tensor that is not of `dtype` on device `dev`."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{what} must live on a CUDA device")
-    if t.dtype != torch.float16:
-        raise TypeError(f"{what} must be torch.float16, got {t.dtype}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{what} is on cuda:{t.get_device()}, others on cuda:{dev}")
+
+
+def _index(t, what):
+    """Index of the CUDA device that a tensor lives on."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what} must be a torch.Tensor")
+    i = t.get_device()
+    if i < 0:
+        raise ValueError(f"{what} must live on a CUDA device")
+    return i
+
+
+def _rows(t, what, dev=None):
+    """(pointer, row stride in elements) of fp16 rows [tokens, heads, head_dim]: the heads of a
+    token are contiguous, the tokens may be any distance apart (a slice of a projection's output)."""
+    if t is None:
+        return None, 0
+    if dev is None:
+        dev = _index(t, what)
+    if t.dtype is not _F16 or t.get_device() != dev:
+        _refuse(t, what, _F16, dev)
     if t.dim() != 3:
         raise ValueError(f"{what} must be [tokens, heads, head_dim], got {tuple(t.shape)}")
     n, h, d = t.shape
-    if (heads is not None and h != heads) or (dim is not None and d != dim):
-        raise ValueError(f"{what} must have {heads} heads of {dim}, got {h} of {d}")
     sn, sh, sd = t.stride()
-    if (sd != 1 and d > 1) or (sh != d and h > 1):
+    if (sh != d and h > 1) or (sd != 1 and d > 1):
         raise ValueError(f"{what}: the heads of a token must be contiguous")
-    if t.numel() == 0:
-        return None, h * d
-    return t.data_ptr(), sn if n > 1 else -(-h * d // 8) * 8
+    if n == 1:
+        sn = -(-h * d // 8) * 8  # the stride of a single row says nothing
+    return t.data_ptr() or None, sn
 
 
-def _same_device(*tensors):
-    """The one device of the tensors given."""
-    dev = None
-    for t in tensors:
-        if t is not None:
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError(f"tensors on {dev} and on {t.device}")
-    return dev
+def _flat(t, what, dtype, dev):
+    """Pointer of a contiguous tensor of `dtype` on device `dev`."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, what, dtype, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr() or None
 
 
 class _on:
-    """Launch on the tensors' device and on `stream` (None: that device's current stream); what is
-    allocated inside belongs to that stream."""
+    """Device `index` and `stream` (None: its current one) as the current ones: what is allocated
+    inside belongs to that stream."""
 
-    def __init__(self, device, stream):
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream of {stream.device}, tensors on {device}")
-        self.contexts = []
-        if device.index is not None and device.index != torch.cuda.current_device():
-            self.contexts.append(torch.cuda.device(device))
+    def __init__(self, index, stream):
+        if stream is not None and stream.device.index != index:
+            raise ValueError(f"stream of {stream.device}, tensors on cuda:{index}")
+        self.contexts = [torch.cuda.device(index)]
         if stream is not None:
             self.contexts.append(torch.cuda.stream(stream))
 
@@ -368,11 +392,12 @@ def _tables(cos, sin, positions, tokens):
         return 0, 0
     if cos is None or sin is None or positions is None:
         raise ValueError("a rotation needs cos, sin and positions")
-    if cos.dim() != 2 or cos.shape != sin.shape:
+    shape = cos.shape
+    if len(shape) != 2 or shape != sin.shape:
         raise ValueError("cos and sin must be [rows, rotary_dim / 2], both alike")
     if positions.shape != (tokens,):
         raise ValueError(f"positions must be [{tokens}], got {tuple(positions.shape)}")
-    return 2 * cos.shape[1], cos.shape[0]
+    return 2 * shape[1], shape[0]
 
 
 def quik_qk_norm_rope(heads, q, k, q_gamma, k_gamma, eps, cos, sin, positions, q_out, k_out,
@@ -654,24 +679,36 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, q_weight=None, k_weigh
     one pass.  q [tokens, q_heads, head_dim] and k fp16, slices of a projection's rows as they are;
     returns (q_out, k_out), new tensors unless given (each may be its input)."""
     n, qh, d = q.shape
-    if k is not None and (k.shape[0] != n or k.shape[2] != d):
-        raise ValueError(f"k must be [{n}, heads, {d}], got {tuple(k.shape)}")
-    kh = 0 if k is None else k.shape[1]
+    kh = 0
+    if k is not None:
+        kn, kh, kd = k.shape
+        if kn != n or kd != d:
+            raise ValueError(f"k must be [{n}, heads, {d}], got {tuple(k.shape)}")
     rotary, rows = _tables(cos, sin, positions, n)
-    for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and w.shape != (d,):
-            raise ValueError(f"{what} must be [{d}], got {tuple(w.shape)}")
-    for o, x, what in ((q_out, q, "q_out"), (k_out, k, "k_out")):
-        if o is not None and (x is None or o.shape != x.shape):
-            raise ValueError(f"{what} must have its input's shape")
-    dev = _same_device(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out)
-    with _on(dev, stream):
-        if q_out is None:
-            q_out = torch.empty((n, qh, d), dtype=torch.float16, device=dev)
-        if k_out is None and k is not None:
-            k_out = torch.empty((n, kh, d), dtype=torch.float16, device=dev)
-        quik_qk_norm_rope(quik_heads(n, qh, kh, d, rotary, bool(interleaved), rows), q, k, q_weight,
-                          k_weight, eps, cos, sin, positions, q_out, k_out)
+    if (q_weight is not None and q_weight.shape != (d,)) or (k_weight is not None and k_weight.shape != (d,)):
+        raise ValueError(f"q_weight and k_weight must be [{d}]")
+    if (q_out is not None and q_out.shape != q.shape) or (k_out is not None and
+                                                          (k is None or k_out.shape != k.shape)):
+        raise ValueError("an output must have its input's shape")
+    dev = _index(q, "q")
+    if stream is not None or dev != _current_device():
+        with _on(dev, stream):
+            return qk_norm_rope(q, k, q_weight, k_weight, eps, cos, sin, positions, interleaved, q_out, k_out)
+    if q_out is None:
+        q_out = q.new_empty((n, qh, d))
+    if k_out is None and k is not None:
+        k_out = k.new_empty((n, kh, d))
+    qp, qs = _rows(q, "q", dev)
+    kp, ks = _rows(k, "k", dev)
+    qo, qos = _rows(q_out, "q_out", dev)
+    ko, kos = _rows(k_out, "k_out", dev)
+    status = (_lib or lib()).quik_qk_norm_rope(
+        quik_heads(n, qh, kh, d, rotary, bool(interleaved), rows), qp, qs, kp, ks,
+        _flat(q_weight, "q_weight", _F16, dev), _flat(k_weight, "k_weight", _F16, dev), eps,
+        _flat(cos, "cos", _F32, dev), _flat(sin, "sin", _F32, dev), _flat(positions, "positions", _I32, dev),
+        qo, qos, ko, kos, _raw_stream(dev))
+    if status:
+        raise QuikError(status, "quik_qk_norm_rope")
     return q_out, k_out
 
 
@@ -695,12 +732,13 @@ class QuikKVCache:
         for s in (k_scale, v_scale):
             if s is not None and s.shape != (pages, heads, page_size):
                 raise ValueError(f"scales must be [{pages}, {heads}, {page_size}], got {tuple(s.shape)}")
-        self.device = _same_device(k, v, k_scale, v_scale)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.heads, self.head_dim, self.page_size, self.pages = heads, row * per, page_size, pages
-        self.struct = quik_kv_cache(kind, heads, row * per, page_size, pages, 0, _ptr(k, k.dtype, "k"),
-                                    _ptr(v, k.dtype, "v"), _ptr(k_scale, torch.float32, "k_scale"),
-                                    _ptr(v_scale, torch.float32, "v_scale"))
+        self.device, self.index = k.device, _index(k, "k")
+        self.struct = quik_kv_cache(kind, heads, row * per, page_size, pages, 0,
+                                    _flat(k, "k", k.dtype, self.index), _flat(v, "v", k.dtype, self.index),
+                                    _flat(k_scale, "k_scale", _F32, self.index),
+                                    _flat(v_scale, "v_scale", _F32, self.index))
 
     @classmethod
     def empty(cls, pages: int, heads: int, head_dim: int, page_size: int = 64, bits: int = 16,
@@ -728,9 +766,18 @@ class QuikKVCache:
         if slots.shape != (n,):
             raise ValueError(f"slots must be [{n}], got {tuple(slots.shape)}")
         rotary, rows = _tables(cos, sin, positions, n)
-        with _on(_same_device(self.k, k, v, slots, cos, sin, positions), stream):
-            quik_kv_append(quik_heads(n, 0, self.heads, self.head_dim, rotary, bool(interleaved), rows),
-                           self.struct, k, v, cos, sin, positions, slots)
+        dev = self.index
+        if stream is not None or dev != _current_device():
+            with _on(dev, stream):
+                return self.append(k, v, slots, cos, sin, positions, interleaved)
+        kp, ks = _rows(k, "k", dev)
+        vp, vs = _rows(v, "v", dev)
+        status = (_lib or lib()).quik_kv_append(
+            quik_heads(n, 0, self.heads, self.head_dim, rotary, bool(interleaved), rows), self.struct, kp, ks,
+            vp, vs, _flat(cos, "cos", _F32, dev), _flat(sin, "sin", _F32, dev),
+            _flat(positions, "positions", _I32, dev), _flat(slots, "slots", _L64, dev), _raw_stream(dev))
+        if status:
+            raise QuikError(status, "quik_kv_append")
 
     def gather(self, slots: torch.Tensor, k_out=None, v_out=None, stream=None):
         """quik_kv_gather: (k, v) fp16 [tokens, heads, head_dim] of slots int64 [tokens]."""
@@ -740,12 +787,20 @@ class QuikKVCache:
         for o in (k_out, v_out):
             if o is not None and o.shape != shape:
                 raise ValueError(f"outputs must be {shape}, got {tuple(o.shape)}")
-        with _on(_same_device(self.k, slots, k_out, v_out), stream):
-            if k_out is None:
-                k_out = torch.empty(shape, dtype=torch.float16, device=self.device)
-            if v_out is None:
-                v_out = torch.empty(shape, dtype=torch.float16, device=self.device)
-            quik_kv_gather(self.struct, slots, k_out, v_out)
+        dev = self.index
+        if stream is not None or dev != _current_device():
+            with _on(dev, stream):
+                return self.gather(slots, k_out, v_out)
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=_F16, device=self.device)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=_F16, device=self.device)
+        kp, ks = _rows(k_out, "k_out", dev)
+        vp, vs = _rows(v_out, "v_out", dev)
+        status = (_lib or lib()).quik_kv_gather(self.struct, shape[0], _flat(slots, "slots", _L64, dev), kp, ks, vp,
+                                                vs, _raw_stream(dev))
+        if status:
+            raise QuikError(status, "quik_kv_gather")
         return k_out, v_out
 
 
@@ -764,25 +819,38 @@ def tree_attention(q: torch.Tensor, cache: QuikKVCache, page_table: torch.Tensor
     n, qh, d = q.shape
     if d != cache.head_dim:
         raise ValueError(f"q must have heads of {cache.head_dim}, got {d}")
-    B = context.numel()
-    if context.dim() != 1 or page_table.dim() != 2 or page_table.shape[0] != B or cu_tokens.shape != (B + 1,):
+    B, width = page_table.shape
+    if context.shape != (B,) or cu_tokens.shape != (B + 1,):
         raise ValueError("context must be [sequences], page_table [sequences, max_pages], cu_tokens "
                          "[sequences + 1]")
-    if mask is not None and (mask.dim() != 2 or mask.shape[0] != n):
-        raise ValueError(f"mask must be [{n}, words], got {tuple(mask.shape)}")
+    words = 0
+    if mask is not None:
+        rows, words = mask.shape
+        if rows != n:
+            raise ValueError(f"mask must be [{n}, words], got {tuple(mask.shape)}")
     if out is not None and out.shape != q.shape:
         raise ValueError("out must have the shape of q")
     if lse is not None and lse.shape != (n, qh):
         raise ValueError(f"lse must be [{n}, {qh}], got {tuple(lse.shape)}")
-    a = quik_attention(n, B, qh, max_tokens, page_table.shape[1], max_context,
-                       0 if mask is None else mask.shape[1], d ** -0.5 if scale is None else scale)
-    dev = _same_device(cache.k, q, page_table, context, cu_tokens, mask, out, lse)
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty((n, qh, d), dtype=torch.float16, device=dev)
-        if lse is None and return_lse:
-            lse = torch.empty((n, qh), dtype=torch.float32, device=dev)
-        need = quik_attention_workspace_size(a, cache.struct)
-        ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
-        quik_tree_attention(a, cache.struct, q, page_table, context, cu_tokens, mask, out, lse, ws)
+    dev = cache.index
+    if stream is not None or dev != _current_device():
+        with _on(dev, stream):
+            return tree_attention(q, cache, page_table, context, cu_tokens, max_tokens, max_context, mask, scale,
+                                  out, lse, return_lse)
+    qp, qs = _rows(q, "q", dev)
+    if out is None:
+        out = q.new_empty((n, qh, d))
+    if lse is None and return_lse:
+        lse = torch.empty((n, qh), dtype=_F32, device=cache.device)
+    op, os_ = _rows(out, "out", dev)
+    a = quik_attention(n, B, qh, max_tokens, width, max_context, words, d ** -0.5 if scale is None else scale)
+    L = _lib or lib()
+    need = L.quik_attention_workspace_size(a, cache.struct)
+    ws = torch.empty(need, dtype=torch.uint8, device=cache.device) if need else None
+    status = L.quik_tree_attention(
+        a, cache.struct, qp, qs, _flat(page_table, "page_table", _I32, dev), _flat(context, "context", _I32, dev),
+        _flat(cu_tokens, "cu_tokens", _I32, dev), _flat(mask, "mask", _I32, dev), op, os_,
+        _flat(lse, "lse", _F32, dev), ws.data_ptr() if need else None, need, _raw_stream(dev))
+    if status:
+        raise QuikError(status, "quik_tree_attention")
     return (out, lse) if return_lse else out
