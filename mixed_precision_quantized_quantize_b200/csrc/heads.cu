@@ -3,16 +3,19 @@
 // V rows to the paged cache (kv_append) and the read-back (kv_gather).
 //
 // A row is one head of one token, D = 64 or 128 channels.  D / 8 lanes hold a
-// row, eight channels (one 16-byte load) each, so a warp holds 4 or 2 rows,
-// and all reductions over a row are shuffles inside that lane group.  The
-// rotation's partner of a channel lies in the same lane (adjacent pairs) or
-// rotary_dim / 2 channels away, a whole number of lanes (rotary_dim % 16 ==
-// 0): one shuffle.  The table entries of a token are loaded once and serve
-// all the rows that a warp takes of that token.
+// row, eight channels each, so a warp holds 4 or 2 rows and all reductions over
+// a row are shuffles inside that lane group.  A lane's eight channels are two
+// runs of four, placed so that both channels of every rotated pair are in the
+// same lane: with pairs (i, i + rotary_dim / 2) a run and the one rotary_dim / 2
+// further on, otherwise two adjacent runs.  The rotation then needs no exchange
+// between lanes.  (With 16-byte loads and the partner's channels shuffled in,
+// norm and rotation of 2048 x 64 heads took 18.6 us.)  The table entries of a
+// token are loaded once and serve all the rows that a warp takes of it.
 //
 // All three kernels are bound by memory: every channel is read once and
-// written once, in 16-byte units.
+// written once.
 #include "quik_internal.h"
+#include "sm100.cuh"
 
 #include <cuda_fp16.h>
 
@@ -24,99 +27,101 @@ __device__ unsigned int g_kv_bad_index;
 
 namespace {
 
-__device__ __forceinline__ uint4 load16(const void *p) {
-    return *reinterpret_cast<const uint4 *>(p);
+using ptx::f2;
+using ptx::f2_add;
+using ptx::f2_fma;
+using ptx::f2_mul;
+using ptx::f2_split;
+using ptx::f2_sub;
+
+__device__ __forceinline__ uint2 load8(const void *p) { return *reinterpret_cast<const uint2 *>(p); }
+__device__ __forceinline__ void store8(void *p, uint2 v) { *reinterpret_cast<uint2 *>(p) = v; }
+
+// Four fp16 channels as two fp32 pairs, and back (rounded to nearest).
+__device__ __forceinline__ void unpack4(uint2 v, uint64_t *x) {
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&v.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&v.y));
+    x[0] = f2(a.x, a.y);
+    x[1] = f2(b.x, b.y);
+}
+__device__ __forceinline__ uint2 pack4(const uint64_t *x) {
+    float a, b;
+    uint2 v;
+    f2_split(x[0], a, b);
+    __half2 h = __floats2half2_rn(a, b);
+    v.x = *reinterpret_cast<const uint32_t *>(&h);
+    f2_split(x[1], a, b);
+    h = __floats2half2_rn(a, b);
+    v.y = *reinterpret_cast<const uint32_t *>(&h);
+    return v;
 }
 
-__device__ __forceinline__ void unpack8(uint4 v, float (&x)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
+// A lane's channels: runs of four at a and b.
+struct Runs {
+    int a, b;
+};
+template <bool INTER>
+__device__ __forceinline__ Runs runs_of(int rotary, int i) {
+    const int half = rotary / 2;
+    Runs r;
+    if (!INTER && 4 * i < half) {
+        r.a = 4 * i;
+        r.b = half + 4 * i;
+    } else {
+        r.a = 8 * i;  // (half-split: the i-th run pair from rotary_dim on is at 2 * 4 i, too)
+        r.b = r.a + 4;
     }
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&h);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    return r;
 }
 
 // The rotation of one token, as this lane needs it: cosines and sines of its
-// channels (adjacent pairs: the first four entries).  In the half-split form
-// the sine carries the sign, so that both halves are own * c + partner * s.
+// four pairs.
 struct Turn {
-    float c[8], s[8];
-    int lanes;  // distance to the partner's lane (half-split)
-    bool on;    // this lane's channels are rotated
+    float c[4], s[4];
+    bool on;  // this lane's channels are rotated
 };
 
 template <bool INTER>
-__device__ __forceinline__ Turn load_turn(const RotaryArgs &r, int token, int e0) {
+__device__ __forceinline__ Turn load_turn(const RotaryArgs &r, int token, int i) {
     Turn t;
-    t.on = e0 < r.rotary;
-    t.lanes = 0;
+    const int half = r.rotary / 2;
+    t.on = 4 * i < half;
     if (r.rotary == 0) return t;
     int pos = r.positions[token];
     if (pos < 0 || pos >= r.rows) {
         if (threadIdx.x % 32 == 0) atomicAdd(&g_kv_bad_index, 1u);
         pos = 0;
     }
-    const int half = r.rotary / 2;
-    const int64_t at = static_cast<int64_t>(pos) * half;
-    if (INTER) {
-        if (t.on) {
-            const float4 c = *reinterpret_cast<const float4 *>(r.cos + at + e0 / 2);
-            const float4 s = *reinterpret_cast<const float4 *>(r.sin + at + e0 / 2);
-            t.c[0] = c.x, t.c[1] = c.y, t.c[2] = c.z, t.c[3] = c.w;
-            t.s[0] = s.x, t.s[1] = s.y, t.s[2] = s.z, t.s[3] = s.w;
-        }
-    } else {
-        const bool low = e0 < half;
-        t.lanes = t.on ? (low ? half / 8 : -(half / 8)) : 0;
-        if (t.on) {
-            const int64_t i = at + (low ? e0 : e0 - half);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float4 c = *reinterpret_cast<const float4 *>(r.cos + i + 4 * h);
-                const float4 s = *reinterpret_cast<const float4 *>(r.sin + i + 4 * h);
-                t.c[4 * h] = c.x, t.c[4 * h + 1] = c.y, t.c[4 * h + 2] = c.z, t.c[4 * h + 3] = c.w;
-                t.s[4 * h] = low ? -s.x : s.x, t.s[4 * h + 1] = low ? -s.y : s.y;
-                t.s[4 * h + 2] = low ? -s.z : s.z, t.s[4 * h + 3] = low ? -s.w : s.w;
-            }
-        }
+    if (t.on) {
+        // pairs 4 i .. 4 i + 3 in both forms
+        const int64_t at = static_cast<int64_t>(pos) * half + 4 * i;
+        const float4 c = *reinterpret_cast<const float4 *>(r.cos + at);
+        const float4 s = *reinterpret_cast<const float4 *>(r.sin + at);
+        t.c[0] = c.x, t.c[1] = c.y, t.c[2] = c.z, t.c[3] = c.w;
+        t.s[0] = s.x, t.s[1] = s.y, t.s[2] = s.z, t.s[3] = s.w;
     }
     return t;
 }
 
-// Rotate x (eight channels of a row) in IEEE steps, each product and each sum
-// rounded: the values (and so the codes made of them) are then the same
-// whatever the compiler would contract.  Every lane of the warp calls it.
+// Rotate a lane's channels x (pairs 0, 1: the run at a; 2, 3: the run at b) in
+// IEEE steps, each product and each sum rounded: the values, and so the codes
+// made of them, are then the same wherever they are computed.  (Paired
+// products followed by a paired sum came out with one rounding instead of two.)
 template <bool INTER>
-__device__ __forceinline__ void rotate(const Turn &t, float (&x)[8]) {
-    if (INTER) {
-        if (t.on) {
+__device__ __forceinline__ void rotate(const Turn &t, uint64_t (&x)[4]) {
+    if (!t.on) return;
+    float v[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float a = x[2 * i], b = x[2 * i + 1];
-                x[2 * i] = __fsub_rn(__fmul_rn(a, t.c[i]), __fmul_rn(b, t.s[i]));
-                x[2 * i + 1] = __fadd_rn(__fmul_rn(b, t.c[i]), __fmul_rn(a, t.s[i]));
-            }
-        }
-    } else {
-        const int src = (threadIdx.x + t.lanes) & 31;
+    for (int i = 0; i < 4; ++i) f2_split(x[i], v[2 * i], v[2 * i + 1]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float o = __shfl_sync(0xffffffffu, x[i], src);
-            if (t.on) x[i] = __fadd_rn(__fmul_rn(x[i], t.c[i]), __fmul_rn(o, t.s[i]));
-        }
+    for (int i = 0; i < 4; ++i) {
+        const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : i + 4;
+        const float a = v[ia], b = v[ib];
+        v[ia] = __fsub_rn(__fmul_rn(a, t.c[i]), __fmul_rn(b, t.s[i]));
+        v[ib] = __fadd_rn(__fmul_rn(b, t.c[i]), __fmul_rn(a, t.s[i]));
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = f2(v[2 * i], v[2 * i + 1]);
 }
 
 // Which token and which rows of it a warp takes: a CTA holds `wt` warps of
@@ -142,58 +147,89 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const QkArgs a, int w
     const int rows = a.q_heads + a.kv_heads;
     const Place p = place<U * RPW>(a.tokens, wt, tpc, rows);
     if (!p.ok) return;
-    const int lane = threadIdx.x % 32, sub = lane / LPR, e0 = lane % LPR * 8;
-    uint4 raw[U];
+    const int lane = threadIdx.x % 32, sub = lane / LPR;
+    const Runs e = runs_of<INTER>(a.rot.rotary, lane % LPR);
+    const uint16_t *q = a.q + p.token * a.q_stride, *k = a.k + p.token * a.k_stride;
+    uint2 raw[U][2];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int r = p.row0 + u * RPW + sub;
-        raw[u] = make_uint4(0, 0, 0, 0);
-        if (r < a.q_heads)
-            raw[u] = load16(a.q + p.token * a.q_stride + r * D + e0);
-        else if (r < rows)
-            raw[u] = load16(a.k + p.token * a.k_stride + (r - a.q_heads) * D + e0);
+        raw[u][0] = raw[u][1] = make_uint2(0, 0);
+        if (r < rows) {
+            const uint16_t *src = r < a.q_heads ? q + r * D : k + (r - a.q_heads) * D;
+            raw[u][0] = load8(src + e.a);
+            raw[u][1] = load8(src + e.b);
+        }
     }
-    const Turn t = load_turn<INTER>(a.rot, p.token, e0);
+    const Turn t = load_turn<INTER>(a.rot, p.token, lane % LPR);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int r = p.row0 + u * RPW + sub;
         const bool is_q = r < a.q_heads;
-        float x[8];
-        unpack8(raw[u], x);
+        uint64_t x[4];
+        unpack4(raw[u][0], x);
+        unpack4(raw[u][1], x + 2);
         const uint16_t *gamma = is_q ? a.q_gamma : a.k_gamma;
         // the sum of squares in fp32: 64 or 128 terms, at most 2^39
-        float ss = 0.0f;
+        uint64_t s2 = f2_mul(x[0], x[0]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+        for (int i = 1; i < 4; ++i) s2 = f2_fma(x[i], x[i], s2);
+        float ss, s1;
+        f2_split(s2, ss, s1);
+        ss += s1;
 #pragma unroll
         for (int m = 1; m < LPR; m *= 2) ss += __shfl_xor_sync(0xffffffffu, ss, m);
         if (gamma != nullptr) {
-            const float rs = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
-            float g[8];
-            unpack8(load16(gamma + e0), g);
+            const float rs = rsqrtf(ss * (1.0f / D) + a.eps);
+            const uint64_t r2 = f2(rs, rs);
+            uint64_t g[4];
+            unpack4(load8(gamma + e.a), g);
+            unpack4(load8(gamma + e.b), g + 2);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = x[i] * rs * g[i];
+            for (int i = 0; i < 4; ++i) x[i] = f2_mul(f2_mul(x[i], r2), g[i]);
         }
         if (a.rot.rotary != 0) rotate<INTER>(t, x);
         if (r < rows) {
-            uint16_t *o = is_q ? a.q_out + p.token * a.q_out_stride + r * D
-                               : a.k_out + p.token * a.k_out_stride + (r - a.q_heads) * D;
-            *reinterpret_cast<uint4 *>(o + e0) = pack8(x);
+            uint16_t *dst = is_q ? a.q_out + p.token * a.q_out_stride + r * D
+                                 : a.k_out + p.token * a.k_out_stride + (r - a.q_heads) * D;
+            store8(dst + e.a, pack4(x));
+            store8(dst + e.b, pack4(x + 2));
         }
     }
 }
 
 // ------------------------------------------------------------------ append
-// rint(v / s) with the IEEE quotient, for |v / s| <= 127 (+ rounding).  The
-// product with the reciprocal is within 127 * 2^-23 of the quotient, so
-// wherever it is further than 1e-4 from a half-integer both round alike; the
-// rest (and every non-finite case, where the comparison fails) divides.
-__device__ __forceinline__ int code_of(float v, float s, float inv, int top) {
-    const float t = v * inv;
-    float q = rintf(t);
-    if (!(fabsf(t - q) <= 0.4999f)) q = rintf(__fdiv_rn(v, s));
-    const int c = __float2int_rn(q);  // NaN gives 0
-    return max(-top, min(top, c));
+// The codes of eight channels.  The product t with the reciprocal is within
+// 127 * 2^-23 = 1.6e-5 of the quotient and the rounded quotient within 0.8e-5
+// of it, so unless t lies within 4e-5 of a half-integer both round alike; t is
+// rounded (half to even) by adding 1.5 * 2^23, whose low mantissa bits then are
+// the code.  One channel in 12500 divides.
+__device__ __forceinline__ void codes_of(const uint64_t (&x)[4], float s, float inv, int top, int (&c)[8]) {
+    const float kRound = 12582912.0f;
+    const uint64_t i2 = f2(inv, inv), k2 = f2(kRound, kRound);
+    float far = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t t = f2_mul(x[i], i2), m = f2_add(t, k2), d = f2_sub(t, f2_sub(m, k2));
+        float a, b;
+        f2_split(m, a, b);
+        c[2 * i] = __float_as_int(a);
+        c[2 * i + 1] = __float_as_int(b);
+        f2_split(d, a, b);
+        far = fmaxf(far, fmaxf(fabsf(a), fabsf(b)));
+    }
+    // outside this range the reciprocal or the products may leave fp32's
+    if (!(far <= 0.49996f && s >= 1e-30f && s <= 1e30f)) {
+        // the IEEE quotient; 0 / 0 and what an infinite or NaN scale gives
+        // convert to zero
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float a, b;
+            f2_split(x[i], a, b);
+            c[2 * i] = max(-top, min(top, __float2int_rn(__fdiv_rn(a, s))));
+            c[2 * i + 1] = max(-top, min(top, __float2int_rn(__fdiv_rn(b, s))));
+        }
+    }
 }
 
 template <int D, bool INTER, int BITS, int U>
@@ -202,79 +238,88 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a, int 
     const int H = a.cache.heads, rows = 2 * H;
     const Place p = place<U * RPW>(a.tokens, wt, tpc, rows);
     if (!p.ok) return;
-    const int lane = threadIdx.x % 32, sub = lane / LPR, e0 = lane % LPR * 8;
+    const int lane = threadIdx.x % 32, sub = lane / LPR;
     const int64_t slot = a.slots[p.token];
     const int64_t limit = static_cast<int64_t>(a.cache.pages) * a.cache.page_size;
     if (slot < 0 || slot >= limit) {  // a padded token, or a slot outside the cache: nothing is written
         if (slot >= limit && lane == 0) atomicAdd(&g_kv_bad_index, 1u);
         return;
     }
-    uint4 raw[U];
+    const Runs e = runs_of<INTER>(a.rot.rotary, lane % LPR);
+    const uint16_t *ks = a.k + p.token * a.k_stride, *vs = a.v + p.token * a.v_stride;
+    uint2 raw[U][2];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int r = p.row0 + u * RPW + sub;
-        raw[u] = make_uint4(0, 0, 0, 0);
-        if (r < H)
-            raw[u] = load16(a.k + p.token * a.k_stride + r * D + e0);
-        else if (r < rows)
-            raw[u] = load16(a.v + p.token * a.v_stride + (r - H) * D + e0);
+        raw[u][0] = raw[u][1] = make_uint2(0, 0);
+        if (r < rows) {
+            const uint16_t *src = r < H ? ks + r * D : vs + (r - H) * D;
+            raw[u][0] = load8(src + e.a);
+            raw[u][1] = load8(src + e.b);
+        }
     }
-    const int64_t page = slot / a.cache.page_size, off = slot % a.cache.page_size;
+    const int shift = __ffs(a.cache.page_size) - 1;  // a power of two
+    const int64_t page = slot >> shift, off = slot & (a.cache.page_size - 1);
     Turn t;
-    const bool any_k = a.rot.rotary != 0 && p.row0 < H;
-    if (any_k) t = load_turn<INTER>(a.rot, p.token, e0);
+    t.on = false;
+    if (a.rot.rotary != 0 && p.row0 < H) t = load_turn<INTER>(a.rot, p.token, lane % LPR);
+    uint64_t x[U][4];
+    float mine = 0.0f;  // of row u where lane % U == u: its largest magnitude
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int r = p.row0 + u * RPW + sub;
+        unpack4(raw[u][0], x[u]);
+        unpack4(raw[u][1], x[u] + 2);
+        if (r < H) rotate<INTER>(t, x[u]);
+        if (BITS == 16) continue;
+        // on the bits NaN > infinity > finite: a row that holds one keeps it in
+        // its scale
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            m = max(m, max(static_cast<uint32_t>(x[u][i]) & 0x7fffffffu,
+                           static_cast<uint32_t>(x[u][i] >> 32) & 0x7fffffffu));
+#pragma unroll
+        for (int s = 1; s < LPR; s *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
+        if (lane % U == u) mine = __uint_as_float(m);
+    }
+    // the two divisions of a row are made by one lane in U
+    constexpr int top = BITS == 4 ? 7 : 127;
+    float scale_u = 0.0f, inv_u = 0.0f;
+    if (BITS != 16) {
+        scale_u = __fdiv_rn(mine, static_cast<float>(top));
+        inv_u = __frcp_rn(scale_u);
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int r = p.row0 + u * RPW + sub;
         const bool is_k = r < H;
-        const int h = is_k ? r : r - H;
-        float x[8];
-        unpack8(raw[u], x);
-        if (any_k) {
-            // a warp may hold rows of both: the shuffles are for all, the result for K
-            float y[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = x[i];
-            rotate<INTER>(t, y);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = is_k ? y[i] : x[i];
-        }
-        const int64_t row = (page * H + h) * a.cache.page_size + off;
+        const int64_t row = (page * H + (is_k ? r : r - H)) * a.cache.page_size + off;
         uint8_t *dst = static_cast<uint8_t *>(is_k ? a.cache.k : a.cache.v) + row * RB;
         if (BITS == 16) {
-            if (r < rows) *reinterpret_cast<uint4 *>(dst + 2 * e0) = pack8(x);
+            if (r < rows) {
+                store8(dst + 2 * e.a, pack4(x[u]));
+                store8(dst + 2 * e.b, pack4(x[u] + 2));
+            }
             continue;
         }
-        // the row's largest magnitude, on the bits: NaN > infinity > finite, so
-        // a row that holds one keeps it in its scale
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
-#pragma unroll
-        for (int s = 1; s < LPR; s *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
-        constexpr int top = BITS == 4 ? 7 : 127;
-        const float scale = __fdiv_rn(__uint_as_float(m), static_cast<float>(top));
-        int c[8] = {};
-        if (scale != 0.0f) {
-            const float inv = __frcp_rn(scale);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) c[i] = code_of(x[i], scale, inv, top);
-        }
+        const int src = (lane & ~(LPR - 1)) | u;
+        const float scale = __shfl_sync(0xffffffffu, scale_u, src);
+        const float inv = __shfl_sync(0xffffffffu, inv_u, src);
         if (r >= rows) continue;
-        if (BITS == 8) {
-            uint32_t w[2];
+        int c[8];
+        codes_of(x[u], scale, inv, top, c);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                w[i] = (c[4 * i] & 255) | (c[4 * i + 1] & 255) << 8 | (c[4 * i + 2] & 255) << 16 |
-                       static_cast<uint32_t>(c[4 * i + 3]) << 24;
-            *reinterpret_cast<uint2 *>(dst + e0) = make_uint2(w[0], w[1]);
-        } else {
-            uint32_t w = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w |= static_cast<uint32_t>(c[i] & 15) << (4 * i);
-            *reinterpret_cast<uint32_t *>(dst + e0 / 2) = w;
+        for (int i = 0; i < 2; ++i) {  // the run at a, the run at b
+            const int *q = c + 4 * i, at = i ? e.b : e.a;
+            if (BITS == 8)
+                *reinterpret_cast<uint32_t *>(dst + at) =
+                    __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+            else
+                *reinterpret_cast<uint16_t *>(dst + at / 2) = static_cast<uint16_t>(
+                    (q[0] & 15) | (q[1] & 15) << 4 | (q[2] & 15) << 8 | (q[3] & 15) << 12);
         }
-        if (e0 == 0) (is_k ? a.cache.k_scale : a.cache.v_scale)[row] = scale;
+        if (lane % LPR == 0) (is_k ? a.cache.k_scale : a.cache.v_scale)[row] = scale;
     }
 }
 
@@ -290,7 +335,8 @@ __global__ void __launch_bounds__(256) kv_gather_kernel(const GatherArgs a, int 
     const int64_t limit = static_cast<int64_t>(a.cache.pages) * a.cache.page_size;
     const bool live = slot >= 0 && slot < limit;
     if (slot >= limit && lane == 0) atomicAdd(&g_kv_bad_index, 1u);
-    const int64_t page = live ? slot / a.cache.page_size : 0, off = live ? slot % a.cache.page_size : 0;
+    const int shift = __ffs(a.cache.page_size) - 1;  // a power of two
+    const int64_t page = live ? slot >> shift : 0, off = live ? slot & (a.cache.page_size - 1) : 0;
     uint4 raw[U];
     float scale[U];
 #pragma unroll
@@ -302,9 +348,9 @@ __global__ void __launch_bounds__(256) kv_gather_kernel(const GatherArgs a, int 
             const bool is_k = r < H;
             const int64_t row = (page * H + (is_k ? r : r - H)) * a.cache.page_size + off;
             const uint8_t *src = static_cast<const uint8_t *>(is_k ? a.cache.k : a.cache.v) + row * RB;
-            if (BITS == 16) raw[u] = load16(src + 2 * e0);
+            if (BITS == 16) raw[u] = *reinterpret_cast<const uint4 *>(src + 2 * e0);
             if (BITS == 8) {
-                const uint2 w = *reinterpret_cast<const uint2 *>(src + e0);
+                const uint2 w = load8(src + e0);
                 raw[u].x = w.x;
                 raw[u].y = w.y;
             }
@@ -318,17 +364,28 @@ __global__ void __launch_bounds__(256) kv_gather_kernel(const GatherArgs a, int 
         if (r >= rows) continue;
         uint4 out = raw[u];
         if (BITS != 16) {
-            float x[8];
+            // a code's bits under the exponent of 2^23 are that plus the
+            // code (offset to be non-negative): no integer conversions
+            uint64_t x[4];
+            const uint64_t s2 = f2(scale[u], scale[u]);
+            const float base = BITS == 8 ? 8388608.0f + 128.0f : 8388608.0f + 8.0f;
+            const uint64_t b2 = f2(base, base);
+            const uint32_t w0 = BITS == 8 ? raw[u].x ^ 0x80808080u : raw[u].x ^ 0x88888888u;
+            const uint32_t w1 = raw[u].y ^ 0x80808080u;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                int c;
-                if (BITS == 8)
-                    c = static_cast<int8_t>((i < 4 ? raw[u].x : raw[u].y) >> (8 * (i % 4)));
-                else
-                    c = static_cast<int>(raw[u].x << (28 - 4 * i)) >> 28;
-                x[i] = __fmul_rn(static_cast<float>(c), scale[u]);
+            for (int i = 0; i < 4; ++i) {
+                uint32_t y[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (BITS == 8)
+                        y[j] = __byte_perm(i < 2 ? w0 : w1, 0x4b000000u, 0x7440 + (2 * i + j) % 4);
+                    else
+                        y[j] = (w0 >> (8 * i + 4 * j) & 15u) | 0x4b000000u;
+                }
+                x[i] = f2_mul(f2_sub(f2(__uint_as_float(y[0]), __uint_as_float(y[1])), b2), s2);
             }
-            out = live ? pack8(x) : make_uint4(0, 0, 0, 0);
+            const uint2 lo = pack4(x), hi = pack4(x + 2);
+            out = live ? make_uint4(lo.x, lo.y, hi.x, hi.y) : make_uint4(0, 0, 0, 0);
         }
         uint16_t *o = r < H ? a.k_out + p.token * a.k_stride + r * D
                             : a.v_out + p.token * a.v_stride + (r - H) * D;
