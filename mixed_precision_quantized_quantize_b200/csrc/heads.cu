@@ -199,13 +199,16 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const QkArgs a, int w
 }
 
 // ------------------------------------------------------------------ append
-// The codes of eight channels.  The product t with the reciprocal is within
-// 127 * 2^-23 = 1.6e-5 of the quotient and the rounded quotient within 0.8e-5
-// of it, so unless t lies within 4e-5 of a half-integer both round alike; t is
-// rounded (half to even) by adding 1.5 * 2^23, whose low mantissa bits then are
-// the code.  One channel in 12500 divides.
-__device__ __forceinline__ void codes_of(const uint64_t (&x)[4], float s, float inv, int top, int (&c)[8]) {
-    const float kRound = 12582912.0f;
+// The codes of eight channels, each in the low bits of its word (INT4: code + 8,
+// which four of add up to a word of nibbles).  The product t with the
+// reciprocal is within 127 * 2^-23 = 1.6e-5 of the quotient and the rounded
+// quotient within 0.8e-5 of it, so unless t lies within 4e-5 of a half-integer
+// both round alike; t is rounded (half to even) by adding 1.5 * 2^23, whose low
+// mantissa bits then are the code.  One channel in 12500 divides.
+template <int BITS>
+__device__ __forceinline__ void codes_of(const uint64_t (&x)[4], float s, float inv, uint32_t (&c)[8]) {
+    constexpr int top = BITS == 4 ? 7 : 127, bias = BITS == 4 ? 8 : 0;
+    const float kRound = 12582912.0f + bias;
     const uint64_t i2 = f2(inv, inv), k2 = f2(kRound, kRound);
     float far = 0.0f;
 #pragma unroll
@@ -213,10 +216,10 @@ __device__ __forceinline__ void codes_of(const uint64_t (&x)[4], float s, float 
         const uint64_t t = f2_mul(x[i], i2), m = f2_add(t, k2), d = f2_sub(t, f2_sub(m, k2));
         float a, b;
         f2_split(m, a, b);
-        c[2 * i] = __float_as_int(a);
-        c[2 * i + 1] = __float_as_int(b);
+        c[2 * i] = __float_as_uint(a);
+        c[2 * i + 1] = __float_as_uint(b);
         f2_split(d, a, b);
-        far = fmaxf(far, fmaxf(fabsf(a), fabsf(b)));
+        far = fmaxf(fmaxf(far, fabsf(a)), fabsf(b));
     }
     // outside this range the reciprocal or the products may leave fp32's
     if (!(far <= 0.49996f && s >= 1e-30f && s <= 1e30f)) {
@@ -226,14 +229,40 @@ __device__ __forceinline__ void codes_of(const uint64_t (&x)[4], float s, float 
         for (int i = 0; i < 4; ++i) {
             float a, b;
             f2_split(x[i], a, b);
-            c[2 * i] = max(-top, min(top, __float2int_rn(__fdiv_rn(a, s))));
-            c[2 * i + 1] = max(-top, min(top, __float2int_rn(__fdiv_rn(b, s))));
+            c[2 * i] = bias + max(-top, min(top, __float2int_rn(__fdiv_rn(a, s))));
+            c[2 * i + 1] = bias + max(-top, min(top, __float2int_rn(__fdiv_rn(b, s))));
         }
     }
 }
 
+// The largest magnitude of eight channels, as bits (non-negative values order
+// alike): NaN > infinity > finite, so a row that holds one keeps it in its
+// scale.  The maximum itself ignores NaN; the sum of products with zero is NaN
+// where a channel is not finite, and the bits are compared then.
+__device__ __forceinline__ uint32_t largest(const uint64_t (&x)[4]) {
+    float m = 0.0f;
+    uint64_t z = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a, b;
+        f2_split(x[i], a, b);
+        m = fmaxf(fmaxf(m, fabsf(a)), fabsf(b));
+        z = f2_fma(x[i], 0ull, z);
+    }
+    uint32_t u = __float_as_uint(m);
+    float z0, z1;
+    f2_split(z, z0, z1);
+    if (z0 + z1 != 0.0f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            u = max(u, max(static_cast<uint32_t>(x[i]) & 0x7fffffffu,
+                           static_cast<uint32_t>(x[i] >> 32) & 0x7fffffffu));
+    }
+    return u;
+}
+
 template <int D, bool INTER, int BITS, int U>
-__global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a, int wt, int tpc) {
+__global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a, int wt, int tpc) {
     constexpr int LPR = D / 8, RPW = 32 / LPR, RB = D * BITS / 8;
     const int H = a.cache.heads, rows = 2 * H;
     const Place p = place<U * RPW>(a.tokens, wt, tpc, rows);
@@ -260,6 +289,8 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a, int 
     }
     const int shift = __ffs(a.cache.page_size) - 1;  // a power of two
     const int64_t page = slot >> shift, off = slot & (a.cache.page_size - 1);
+    const int64_t row0 = ((page * H) << shift) + off;  // the token's row of head 0
+    uint8_t *kd = static_cast<uint8_t *>(a.cache.k) + row0 * RB, *vd = static_cast<uint8_t *>(a.cache.v) + row0 * RB;
     Turn t;
     t.on = false;
     if (a.rot.rotary != 0 && p.row0 < H) t = load_turn<INTER>(a.rot, p.token, lane % LPR);
@@ -272,13 +303,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a, int 
         unpack4(raw[u][1], x[u] + 2);
         if (r < H) rotate<INTER>(t, x[u]);
         if (BITS == 16) continue;
-        // on the bits NaN > infinity > finite: a row that holds one keeps it in
-        // its scale
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            m = max(m, max(static_cast<uint32_t>(x[u][i]) & 0x7fffffffu,
-                           static_cast<uint32_t>(x[u][i] >> 32) & 0x7fffffffu));
+        uint32_t m = largest(x[u]);
 #pragma unroll
         for (int s = 1; s < LPR; s *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
         if (lane % U == u) mine = __uint_as_float(m);
@@ -294,8 +319,8 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a, int 
     for (int u = 0; u < U; ++u) {
         const int r = p.row0 + u * RPW + sub;
         const bool is_k = r < H;
-        const int64_t row = (page * H + (is_k ? r : r - H)) * a.cache.page_size + off;
-        uint8_t *dst = static_cast<uint8_t *>(is_k ? a.cache.k : a.cache.v) + row * RB;
+        const int at_head = (is_k ? r : r - H) << shift;  // rows from the token's first head
+        uint8_t *dst = (is_k ? kd : vd) + at_head * RB;
         if (BITS == 16) {
             if (r < rows) {
                 store8(dst + 2 * e.a, pack4(x[u]));
@@ -307,19 +332,20 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a, int 
         const float scale = __shfl_sync(0xffffffffu, scale_u, src);
         const float inv = __shfl_sync(0xffffffffu, inv_u, src);
         if (r >= rows) continue;
-        int c[8];
-        codes_of(x[u], scale, inv, top, c);
+        uint32_t c[8];
+        codes_of<BITS>(x[u], scale, inv, c);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {  // the run at a, the run at b
-            const int *q = c + 4 * i, at = i ? e.b : e.a;
+            const uint32_t *q = c + 4 * i;
+            const int at = i ? e.b : e.a;
             if (BITS == 8)
                 *reinterpret_cast<uint32_t *>(dst + at) =
                     __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
-            else
-                *reinterpret_cast<uint16_t *>(dst + at / 2) = static_cast<uint16_t>(
-                    (q[0] & 15) | (q[1] & 15) << 4 | (q[2] & 15) << 8 | (q[3] & 15) << 12);
+            else  // 8 more in every nibble is its top bit flipped
+                *reinterpret_cast<uint16_t *>(dst + at / 2) =
+                    static_cast<uint16_t>((q[0] + q[1] * 16 + q[2] * 256 + q[3] * 4096) ^ 0x8888u);
         }
-        if (lane % LPR == 0) (is_k ? a.cache.k_scale : a.cache.v_scale)[row] = scale;
+        if (lane % LPR == 0) (is_k ? a.cache.k_scale : a.cache.v_scale)[row0 + at_head] = scale;
     }
 }
 
@@ -337,6 +363,9 @@ __global__ void __launch_bounds__(256) kv_gather_kernel(const GatherArgs a, int 
     if (slot >= limit && lane == 0) atomicAdd(&g_kv_bad_index, 1u);
     const int shift = __ffs(a.cache.page_size) - 1;  // a power of two
     const int64_t page = live ? slot >> shift : 0, off = live ? slot & (a.cache.page_size - 1) : 0;
+    const int64_t row0 = ((page * H) << shift) + off;  // the token's row of head 0
+    const uint8_t *kd = static_cast<const uint8_t *>(a.cache.k) + row0 * RB;
+    const uint8_t *vd = static_cast<const uint8_t *>(a.cache.v) + row0 * RB;
     uint4 raw[U];
     float scale[U];
 #pragma unroll
@@ -346,8 +375,8 @@ __global__ void __launch_bounds__(256) kv_gather_kernel(const GatherArgs a, int 
         scale[u] = 0.0f;
         if (r < rows && live) {
             const bool is_k = r < H;
-            const int64_t row = (page * H + (is_k ? r : r - H)) * a.cache.page_size + off;
-            const uint8_t *src = static_cast<const uint8_t *>(is_k ? a.cache.k : a.cache.v) + row * RB;
+            const int at_head = (is_k ? r : r - H) << shift;
+            const uint8_t *src = (is_k ? kd : vd) + at_head * RB;
             if (BITS == 16) raw[u] = *reinterpret_cast<const uint4 *>(src + 2 * e0);
             if (BITS == 8) {
                 const uint2 w = load8(src + e0);
@@ -355,7 +384,7 @@ __global__ void __launch_bounds__(256) kv_gather_kernel(const GatherArgs a, int 
                 raw[u].y = w.y;
             }
             if (BITS == 4) raw[u].x = *reinterpret_cast<const uint32_t *>(src + e0 / 2);
-            if (BITS != 16) scale[u] = (is_k ? a.cache.k_scale : a.cache.v_scale)[row];
+            if (BITS != 16) scale[u] = (is_k ? a.cache.k_scale : a.cache.v_scale)[row0 + at_head];
         }
     }
 #pragma unroll
@@ -364,26 +393,33 @@ __global__ void __launch_bounds__(256) kv_gather_kernel(const GatherArgs a, int 
         if (r >= rows) continue;
         uint4 out = raw[u];
         if (BITS != 16) {
-            // a code's bits under the exponent of 2^23 are that plus the
-            // code (offset to be non-negative): no integer conversions
-            uint64_t x[4];
-            const uint64_t s2 = f2(scale[u], scale[u]);
-            const float base = BITS == 8 ? 8388608.0f + 128.0f : 8388608.0f + 8.0f;
-            const uint64_t b2 = f2(base, base);
-            const uint32_t w0 = BITS == 8 ? raw[u].x ^ 0x80808080u : raw[u].x ^ 0x88888888u;
-            const uint32_t w1 = raw[u].y ^ 0x80808080u;
+            // a code's bits (offset to be non-negative) under the exponent of
+            // 2^10, or four bits up of 2^6, of an fp16: that plus the code
+            uint32_t h[4];
+            if (BITS == 8) {
+                const uint32_t w0 = raw[u].x ^ 0x80808080u, w1 = raw[u].y ^ 0x80808080u;
+                h[0] = __byte_perm(w0, 0x64006400u, 0x5150), h[1] = __byte_perm(w0, 0x64006400u, 0x5352);
+                h[2] = __byte_perm(w1, 0x64006400u, 0x5150), h[3] = __byte_perm(w1, 0x64006400u, 0x5352);
+            } else {  // pairs (0, 4), (1, 5), (2, 6), (3, 7)
+                const uint32_t w = raw[u].x, y = w >> 8;
+                h[0] = ((w ^ 0x88888888u) & 0x000f000fu) | 0x64006400u;
+                h[1] = ((w ^ 0x88888888u) & 0x00f000f0u) | 0x54005400u;
+                h[2] = ((y ^ 0x88888888u) & 0x000f000fu) | 0x64006400u;
+                h[3] = ((y ^ 0x88888888u) & 0x00f000f0u) | 0x54005400u;
+            }
+            float f[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint32_t y[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if (BITS == 8)
-                        y[j] = __byte_perm(i < 2 ? w0 : w1, 0x4b000000u, 0x7440 + (2 * i + j) % 4);
-                    else
-                        y[j] = (w0 >> (8 * i + 4 * j) & 15u) | 0x4b000000u;
-                }
-                x[i] = f2_mul(f2_sub(f2(__uint_as_float(y[0]), __uint_as_float(y[1])), b2), s2);
+                const float base = BITS == 8 ? 1152.0f : i % 2 ? 72.0f : 1032.0f;
+                const float2 v = __half22float2(__hsub2(*reinterpret_cast<const __half2 *>(&h[i]),
+                                                        __float2half2_rn(base)));
+                f[BITS == 8 ? 2 * i : i] = v.x;
+                f[BITS == 8 ? 2 * i + 1 : i + 4] = v.y;
             }
+            uint64_t x[4];
+            const uint64_t s2 = f2(scale[u], scale[u]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = f2_mul(f2(f[2 * i], f[2 * i + 1]), s2);
             const uint2 lo = pack4(x), hi = pack4(x + 2);
             out = live ? make_uint4(lo.x, lo.y, hi.x, hi.y) : make_uint4(0, 0, 0, 0);
         }
