@@ -14,7 +14,7 @@ constexpr int kMaxDevices = 64;
 std::atomic<int> g_sm_count[kMaxDevices];
 // (kernel, device) pairs already configured; a fixed table, so that launches
 // never allocate host memory either.
-constexpr int kMaxKernels = 64;
+constexpr int kMaxKernels = 128;
 std::mutex g_attr_mu;
 const void *g_attr_kernel[kMaxKernels];
 unsigned long long g_attr_devmask[kMaxKernels];

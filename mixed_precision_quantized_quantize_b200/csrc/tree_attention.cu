@@ -122,23 +122,19 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[BYTES / 4], uint32_t ad
         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
 }
 
-// Codes to fp16, exactly: a code's bits (offset to be non-negative) are put
-// into the mantissa of 2^10 (or, four bits up, of 2^6), and that base plus the
-// offset is subtracted.
-constexpr uint32_t kBase8 = 0x64006400u;    // 1024, 1024
-constexpr uint32_t kSub8 = 0x64806480u;     // 1024 + 128
-constexpr uint32_t kBase4 = 0x64006400u;    // 1024: nibble in bits 0-3
-constexpr uint32_t kSub4 = 0x64086408u;     // 1024 + 8
-constexpr uint32_t kBase4Up = 0x54005400u;  // 64: nibble in bits 4-7
-constexpr uint32_t kSub4Up = 0x54805480u;   // 64 + 8
-// bytes 0, 1 (hi: 2, 3) of x (already ^ 0x80) as a pair
+// Codes to fp16, exactly: a code's bits, its sign bit flipped (that adds 128 or
+// 8), are put into the mantissa of 2^10 (or, four bits up, of 2^6), and that
+// base plus the offset is subtracted.  (Without the subtraction, the codes as
+// fp16 subnormals and the offset taken off the sums, a product lost up to ten
+// bits: the tensor cores align subnormals by their nominal exponent.)
+// bytes 0, 1 (hi: 2, 3) of x, already ^ 0x80808080, as a pair
 __device__ __forceinline__ uint32_t pair8(uint32_t x, bool hi) {
-    return half2_sub(pick(x, kBase8, hi ? 0x5352u : 0x5150u), kSub8);
+    return half2_sub(pick(x, 0x64006400u, hi ? 0x5352u : 0x5150u), 0x64806480u);  // 1024 + 128
 }
-// the nibbles at bits 0 and 16 (up: 4 and 20) of x (already ^ 8) as a pair
+// the nibbles at bits 0 and 16 (up: 4 and 20) of x as a pair
 __device__ __forceinline__ uint32_t pair4(uint32_t x, bool up) {
-    return up ? half2_sub((x & 0x00f000f0u) | kBase4Up, kSub4Up)
-              : half2_sub((x & 0x000f000fu) | kBase4, kSub4);
+    const uint32_t c = up ? 0x54805480u : 0x64086408u;  // 64 + 8, 1024 + 8
+    return half2_sub((x & (up ? 0x00f000f0u : 0x000f000fu)) ^ c, c);
 }
 
 // WR warps share a tile, 16 rows each; NW / WR such groups take tiles in turn.
@@ -187,6 +183,143 @@ __device__ __forceinline__ Seq sequence(const Params &p, int b, bool report) {
     if (bad && report) atomicAdd(&g_attn_bad_index, 1u);
     s.total = bad ? 0 : static_cast<int>(total);
     return s;
+}
+
+// The cached rows of one sequence and key head, tile by tile, into a ring of
+// stages in shared memory.  TH threads (a warp, or the WR warps that share a
+// tile) copy together.  Pages hold 16 tokens or more, so each half of a tile is
+// contiguous in memory: two row offsets, one page number each, place it all.
+template <class C>
+struct Tiles {
+    static constexpr int TH = 32 * C::WR;
+    const uint8_t *k, *v;
+    const float *ks, *vs;
+    const int32_t *table;
+    uint8_t *ring;
+    int page_shift, pages, heads, h, end, total;
+    int gt;  // thread among the TH
+    bool report;
+
+    // Page of the half of the tile that this lane stands for (lanes 0-15, 16-31); -1: none.
+    __device__ __forceinline__ int page_of(int tile) const {
+        const int pos = tile * kTile + (threadIdx.x & 16);
+        if (tile >= end || pos >= total) return -1;
+        const int id = table[pos >> page_shift];
+        if (id >= 0 && id < pages) return id;
+        if (report && (threadIdx.x & 15) == 0) atomicAdd(&g_attn_bad_index, 1u);
+        return -1;
+    }
+    // Start the copies of a tile (id: page_of of it).
+    __device__ __forceinline__ void issue(int tile, int stage, int id) const {
+        uint8_t *st = ring + stage * C::STAGE;
+        const uint32_t ka = smem_addr(st), va = ka + kTile * C::KS;
+        const int left = total - tile * kTile;  // tokens from the tile's first one on
+        int64_t row[2];
+        bool have[2];
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            const int pid = __shfl_sync(0xffffffffu, id, 16 * f);
+            have[f] = pid >= 0;
+            row[f] = ((static_cast<int64_t>(have[f] ? pid : 0) * heads + h) << page_shift) +
+                     ((tile * kTile + 16 * f) & ((1 << page_shift) - 1));
+        }
+        constexpr int N = kTile * C::CPR, HALF = N / 2;
+#pragma unroll
+        for (int i = 0; i < (N + TH - 1) / TH; ++i) {
+            const int x = i * TH + gt, t = x / C::CPR, c = x % C::CPR;
+            if (N % TH != 0 && x >= N) break;
+            const bool second = HALF % TH == 0 ? i * TH >= HALF : x >= HALF;
+            const bool ok = (second ? have[1] : have[0]) && t < left;
+            // (x - HALF) * 16 = (t - 16) * RB + 16 c: the half's own offset
+            const int64_t off = (second ? row[1] * C::RB + (x - HALF) * 16 : row[0] * C::RB + x * 16);
+            copy16(ka + t * C::KS + c * 16, k + (ok ? off : 0), ok);
+            copy16(va + t * C::VS + c * 16, v + (ok ? off : 0), ok);
+        }
+        if (gt < 32) {
+            uint8_t *tail = st + kTile * (C::KS + C::VS);
+            const bool second = gt >= 16, ok = (second ? have[1] : have[0]) && gt < left;
+            if constexpr (C::BITS != 16) {
+                const int64_t r = second ? row[1] + (gt - 16) : row[0] + gt;
+                copy4(smem_addr(tail) + 4 * gt, ks + (ok ? r : 0), ok);
+                copy4(smem_addr(tail) + 4 * (kTile + gt), vs + (ok ? r : 0), ok);
+            }
+            const unsigned live = __ballot_sync(0xffffffffu, ok);
+            if (gt == 0) *reinterpret_cast<unsigned *>(tail + C::SCALES) = live;
+        }
+    }
+};
+
+template <class C>
+__device__ __forceinline__ Tiles<C> tiles_of(const Params &p, const Seq &sq, int b, int h, int end, uint8_t *ring,
+                                             int gt, bool report) {
+    Tiles<C> t;
+    t.k = p.k, t.v = p.v, t.ks = p.ks, t.vs = p.vs;
+    t.table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
+    t.ring = ring;
+    t.page_shift = p.page_shift, t.pages = p.pages, t.heads = p.heads, t.h = h;
+    t.end = end, t.total = sq.total, t.gt = gt, t.report = report;
+    return t;
+}
+
+// Which of the 32 tokens from new token j0 on (negative: context) new token
+// `tok` sees; tok < 0 (no such row): all of them.
+__device__ __forceinline__ unsigned seen(const Params &p, int first, int tok, int j0) {
+    if (tok < 0 || j0 + kTile <= 0) return 0xffffffffu;
+    if (p.mask == nullptr) {
+        const int top = tok - j0;  // last visible position of the tile
+        return top < 0 ? 0u : top >= 31 ? 0xffffffffu : (2u << top) - 1u;
+    }
+    const uint32_t *row = p.mask + static_cast<int64_t>(first + tok) * p.mask_words;
+    if (j0 < 0) return (row[0] << -j0) | ((1u << -j0) - 1u);
+    const int w = j0 / 32;
+    const uint32_t lo = w < p.mask_words ? row[w] : 0u;
+    const uint32_t hi = w + 1 < p.mask_words ? row[w + 1] : 0u;
+    return __funnelshift_r(lo, hi, j0 % 32);
+}
+
+// The unit of the values' scales: the exponent above the largest finite one
+// (given by its bits).
+__device__ __forceinline__ int top_exponent(unsigned top) {
+    return min(max(static_cast<int>(top >> 23) - 126, -100), 126);
+}
+__device__ __forceinline__ unsigned finite_bits(float x) {
+    const unsigned u = __float_as_uint(x) & 0x7fffffffu;
+    return u < 0x7f800000u ? u : 0u;
+}
+
+// Four channels from d on of row r of a block (row g of its sequence): the
+// warp groups' results, `step` rows apart in shared memory, joined and written.
+template <class C>
+__device__ __forceinline__ void finish_row(const Params &p, const Seq &sq, const uint8_t *smem, int split, int h,
+                                           int g, int r, int step, int groups, int d) {
+    const float *mo = reinterpret_cast<const float *>(smem);
+    const float2 *ml = reinterpret_cast<const float2 *>(smem + groups * step * C::OP * 4);
+    float M = -INFINITY;
+    for (int k = 0; k < groups; ++k) M = fmaxf(M, ml[k * step + r].x);
+    const float base = M == -INFINITY ? 0.0f : M;
+    float L = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int k = 0; k < groups; ++k) {
+        const float2 a = ml[k * step + r];
+        const float f = exp2_fast(a.x - base);
+        const float4 v = *reinterpret_cast<const float4 *>(mo + (k * step + r) * C::OP + d);
+        L = fmaf(f, a.y, L);
+        acc.x = fmaf(f, v.x, acc.x), acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z), acc.w = fmaf(f, v.w, acc.w);
+    }
+    const int head = h * p.group + g % p.group, token = sq.first + g / p.group;
+    const int64_t row = static_cast<int64_t>(token) * p.q_heads + head;
+    if (p.splits == 1) {
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+        *reinterpret_cast<uint2 *>(p.out + static_cast<int64_t>(token) * p.out_stride + head * C::D + d) =
+            make_uint2(half2_of(acc.x * inv, acc.y * inv), half2_of(acc.z * inv, acc.w * inv));
+        if (d == 0 && p.lse != nullptr)
+            p.lse[row] = L == 0.0f ? -INFINITY : (M - kShift + log2f(L)) * 0.693147180559945f;
+    } else {
+        const int64_t at = static_cast<int64_t>(split) * p.tokens * p.q_heads + row;
+        *reinterpret_cast<float4 *>(p.part_o + at * C::D + d) = acc;
+        if (d == 0) p.part_ml[at] = make_float2(M, L);
+    }
 }
 
 template <class C>
@@ -248,50 +381,9 @@ __global__ void __launch_bounds__(C::NW * 32) tree_attention_kernel(const Params
         }
     }
 
-    // ---- copies of a tile
-    uint8_t *ring = smem + tg * C::STAGES * C::STAGE;
-    const int32_t *table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
-    const int page_mask = (1 << p.page_shift) - 1;
-    auto page_of = [&](int tile) -> int {  // of token `lane` of the tile; -1: none
-        const int pos = tile * kTile + lane;
-        if (tile >= t1 || pos >= sq.total) return -1;
-        const int id = table[pos >> p.page_shift];
-        if (id >= 0 && id < p.pages) return id;
-        if (wr == 0 && rb == 0) atomicAdd(&g_attn_bad_index, 1u);
-        return -1;
-    };
-    auto issue = [&](int tile, int stage, int id) {
-        uint8_t *st = ring + stage * C::STAGE;
-        const uint32_t ka = smem_addr(st), va = ka + kTile * C::KS;
-        const unsigned live = __ballot_sync(0xffffffffu, id >= 0);
-        constexpr int TH = 32 * WR;
-        const int gt = wr * 32 + lane;
-#pragma unroll
-        for (int i = 0; i < (kTile * C::CPR + TH - 1) / TH; ++i) {
-            const int x = i * TH + gt, t = x / C::CPR, c = x % C::CPR;
-            const int pid = __shfl_sync(0xffffffffu, id, t & 31);
-            const bool ok = pid >= 0;
-            const int64_t row = ((static_cast<int64_t>(ok ? pid : 0) * p.heads + h) << p.page_shift) +
-                                ((tile * kTile + t) & page_mask);
-            const int64_t off = ok ? row * C::RB + c * 16 : 0;
-            if (kTile * C::CPR % TH == 0 || x < kTile * C::CPR) {
-                copy16(ka + t * C::KS + c * 16, p.k + off, ok);
-                copy16(va + t * C::VS + c * 16, p.v + off, ok);
-            }
-        }
-        uint8_t *tail = st + kTile * (C::KS + C::VS);
-        if (wr == 0) {
-            if constexpr (BITS != 16) {
-                const bool ok = id >= 0;
-                const int64_t row = ((static_cast<int64_t>(ok ? id : 0) * p.heads + h) << p.page_shift) +
-                                    ((tile * kTile + lane) & page_mask);
-                copy4(smem_addr(tail) + 4 * lane, p.ks + (ok ? row : 0), ok);
-                copy4(smem_addr(tail) + 4 * (kTile + lane), p.vs + (ok ? row : 0), ok);
-            }
-            if (lane == 0) *reinterpret_cast<unsigned *>(tail + C::SCALES) = live;
-        }
-    };
-
+    const Tiles<C> src = tiles_of<C>(p, sq, b, h, t1, smem + tg * C::STAGES * C::STAGE, wr * 32 + lane,
+                                     wr == 0 && rb == 0);
+    uint8_t *ring = src.ring;
     float o[C::NT][4];
 #pragma unroll
     for (int i = 0; i < C::NT; ++i)
@@ -301,13 +393,13 @@ __global__ void __launch_bounds__(C::NW * 32) tree_attention_kernel(const Params
     int R = -100;  // exponent of the unit of o (quantised values)
 
     int next = t0 + tg;  // tile to be issued next, and its pages
-    int id = page_of(next);
+    int id = src.page_of(next);
 #pragma unroll
     for (int s = 0; s < C::STAGES - 1; ++s) {
-        if (next < t1) issue(next, s, id);
+        if (next < t1) src.issue(next, s, id);
         copy_commit();
         next += TG;
-        id = page_of(next);
+        id = src.page_of(next);
     }
 
     int stage = 0;
@@ -317,10 +409,10 @@ __global__ void __launch_bounds__(C::NW * 32) tree_attention_kernel(const Params
         {
             int free_stage = stage + C::STAGES - 1;
             if (free_stage >= C::STAGES) free_stage -= C::STAGES;
-            if (next < t1) issue(next, free_stage, id);
+            if (next < t1) src.issue(next, free_stage, id);
             copy_commit();
             next += TG;
-            id = page_of(next);
+            id = src.page_of(next);
         }
         const uint8_t *st = ring + stage * C::STAGE;
         const uint32_t ka = smem_addr(st), va = ka + kTile * C::KS;
@@ -354,7 +446,7 @@ __global__ void __launch_bounds__(C::NW * 32) tree_attention_kernel(const Params
                             const uint32_t x = w[i] ^ 0x80808080u;
                             mma(s[n], qf[u * (UB / 4) + i], pair8(x, false), pair8(x, true));
                         } else {
-                            const uint32_t x = w[i] ^ 0x88888888u, y = x >> 8;
+                            const uint32_t x = w[i], y = x >> 8;
                             const int k = 2 * (u * (UB / 4) + i);
                             mma(s[n], qf[k], pair4(x, false), pair4(x, true));
                             mma(s[n], qf[k + 1], pair4(y, false), pair4(y, true));
@@ -381,30 +473,8 @@ __global__ void __launch_bounds__(C::NW * 32) tree_attention_kernel(const Params
         unsigned see[2] = {live, live};
         const bool masked = live != 0xffffffffu || j0 + kTile > 0;
         if (masked) {
-            if (j0 + kTile > 0) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    unsigned bits = 0;
-                    if (tok[e] < 0) {
-                        bits = 0xffffffffu;
-                    } else if (p.mask == nullptr) {
-                        const int top = tok[e] - j0;  // last visible position of the tile
-                        bits = top < 0 ? 0u : top >= 31 ? 0xffffffffu : (2u << top) - 1u;
-                    } else {
-                        const uint32_t *row =
-                            p.mask + static_cast<int64_t>(sq.first + tok[e]) * p.mask_words;
-                        if (j0 < 0) {
-                            bits = (row[0] << -j0) | ((1u << -j0) - 1u);
-                        } else {
-                            const int w = j0 / 32, sh = j0 % 32;
-                            const uint32_t lo = w < p.mask_words ? row[w] : 0u;
-                            const uint32_t hi = w + 1 < p.mask_words ? row[w + 1] : 0u;
-                            bits = __funnelshift_r(lo, hi, sh);
-                        }
-                    }
-                    see[e] &= bits;
-                }
-            }
+            see[0] &= seen(p, sq.first, tok[0], j0);
+            see[1] &= seen(p, sq.first, tok[1], j0);
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
@@ -433,13 +503,10 @@ __global__ void __launch_bounds__(C::NW * 32) tree_attention_kernel(const Params
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const unsigned u = __float_as_uint(vsc[n][e]) & 0x7fffffffu;
-                    top = max(top, u < 0x7f800000u ? u : 0u);
-                }
+                for (int e = 0; e < 2; ++e) top = max(top, finite_bits(vsc[n][e]));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int e = min(max(static_cast<int>(top >> 23) - 126, -100), 126);
+            const int e = top_exponent(top);
             if (e > R) {
                 const float f = exp2_fast(static_cast<float>(R - e));
                 alpha[0] *= f, alpha[1] *= f;
@@ -561,8 +628,8 @@ __global__ void __launch_bounds__(C::NW * 32) tree_attention_kernel(const Params
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
                             const uint32_t sel = y ? 0x7632u : 0x5410u;
-                            const uint32_t a = pick(w[0][i], w[1][i], sel) ^ 0x88888888u, a2 = a >> 8;
-                            const uint32_t c = pick(w[2][i], w[3][i], sel) ^ 0x88888888u, c2 = c >> 8;
+                            const uint32_t a = pick(w[0][i], w[1][i], sel), a2 = a >> 8;
+                            const uint32_t c = pick(w[2][i], w[3][i], sel), c2 = c >> 8;
                             mma(o[8 * i + 4 * y], pf[k], pair4(a, false), pair4(c, false));
                             mma(o[8 * i + 4 * y + 1], pf[k], pair4(a, true), pair4(c, true));
                             mma(o[8 * i + 4 * y + 2], pf[k], pair4(a2, false), pair4(c2, false));
@@ -598,36 +665,376 @@ __global__ void __launch_bounds__(C::NW * 32) tree_attention_kernel(const Params
         const int r = x / (D / 4), d = x % (D / 4) * 4;
         const int g = rb * C::ROWS + r;
         if (g >= rows) break;
-        float M = -INFINITY;
+        finish_row<C>(p, sq, smem, split, h, g, r, C::ROWS, TG, d);
+    }
+}
+
+// ------------------------------------------------------------------ up to 8 rows
+// The transposed products, S^T = K Q^T and O^T = V^T P^T: with the cached
+// tokens (then the channels) as the 16 rows of an m16n8k16 product and the
+// query rows as its 8 columns, a decoding step's few rows cost half the
+// products, accumulators and exponentials.  P^T turns from the accumulators'
+// layout into the second product's operand by movmatrix.
+template <int BITS_, int D_>
+struct FewCfg {
+    static constexpr int BITS = BITS_, D = D_, WR = 1, NW = 4, TG = 4, ROWS = 8;
+    static constexpr int RB = D * BITS / 8, CPR = RB / 16;
+    static constexpr int KS = RB >= 128 ? RB + 16 : RB, VS = RB + 16;
+    static constexpr int SCALES = BITS == 16 ? 0 : 2 * kTile * 4;
+    static constexpr int STAGE = kTile * (KS + VS) + SCALES + 16;
+    static constexpr int STAGES = STAGE > 4000 && STAGE < 6000 ? 2 : 3;
+    static constexpr int RING = TG * STAGES * STAGE;
+    static constexpr int OP = D + 4;
+    static constexpr int MERGE = NW * ROWS * OP * 4 + NW * ROWS * 8;
+    static constexpr int SMEM = RING > MERGE ? RING : MERGE;
+    static constexpr int STEPS = D / 16, MT = D / 16;
+};
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+template <class C>
+__global__ void __launch_bounds__(C::NW * 32, C::BITS == 4 ? 5 : 4) tree_attention_few_kernel(const Params p) {
+    constexpr int BITS = C::BITS, D = C::D, TG = C::TG;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int split = blockIdx.x % p.splits, rb = blockIdx.x / p.splits;
+    const int h = blockIdx.y, b = blockIdx.z;
+    const Seq sq = sequence(p, b, blockIdx.x == 0 && h == 0 && threadIdx.x == 0);
+    const int rows = sq.n * p.group;
+    if (rb * C::ROWS >= rows) return;
+    const int tiles = (sq.total + kTile - 1) / kTile;
+    const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * split / p.splits);
+    const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / p.splits);
+
+    const Tiles<C> src = tiles_of<C>(p, sq, b, h, t1, smem + warp * C::STAGES * C::STAGE, lane, rb == 0);
+    int next = t0 + warp;
+    int id = src.page_of(next);
 #pragma unroll
-        for (int k = 0; k < TG; ++k) M = fmaxf(M, ml[(k * WR + r / 16) * 16 + r % 16].x);
-        const float base = M == -INFINITY ? 0.0f : M;
-        float L = 0.0f;
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int s = 0; s < C::STAGES - 1; ++s) {
+        if (next < t1) src.issue(next, s, id);
+        copy_commit();
+        next += TG;
+        id = src.page_of(next);
+    }
+
+    // ---- the query rows as the products' second operand: this lane's is row
+    // q8, and of it the channels that the lanes' K words give up together
+    const int q4 = lane & 3, q8 = lane >> 2;
+    uint32_t qf[C::STEPS][2];
+    {
+        const int r = rb * C::ROWS + q8;
+        const bool ok = r < rows;
+        const uint16_t *row = p.q;
+        if (ok)
+            row += static_cast<int64_t>(sq.first + r / p.group) * p.q_stride +
+                   static_cast<int64_t>(h * p.group + r % p.group) * D;
+        if constexpr (BITS == 16) {
 #pragma unroll
-        for (int k = 0; k < TG; ++k) {
-            const int w = k * WR + r / 16;
-            const float2 a = ml[w * 16 + r % 16];
-            const float f = exp2_fast(a.x - base);
-            const float4 v = *reinterpret_cast<const float4 *>(
-                reinterpret_cast<const float *>(smem) + (w * 16 + r % 16) * C::OP + d);
-            L = fmaf(f, a.y, L);
-            acc.x = fmaf(f, v.x, acc.x), acc.y = fmaf(f, v.y, acc.y);
-            acc.z = fmaf(f, v.z, acc.z), acc.w = fmaf(f, v.w, acc.w);
-        }
-        const int head = h * p.group + g % p.group, token = sq.first + g / p.group;
-        const int64_t row = static_cast<int64_t>(token) * p.q_heads + head;
-        if (p.splits == 1) {
-            const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-            *reinterpret_cast<uint2 *>(p.out + static_cast<int64_t>(token) * p.out_stride + head * D + d) =
-                make_uint2(half2_of(acc.x * inv, acc.y * inv), half2_of(acc.z * inv, acc.w * inv));
-            if (d == 0 && p.lse != nullptr)
-                p.lse[row] = L == 0.0f ? -INFINITY : (M - kShift + log2f(L)) * 0.693147180559945f;
+            for (int s = 0; s < C::STEPS; ++s)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    qf[s][x] = ok ? *reinterpret_cast<const uint32_t *>(row + 16 * s + 8 * x + 2 * q4) : 0u;
         } else {
-            const int64_t at = static_cast<int64_t>(split) * p.tokens * p.q_heads + row;
-            *reinterpret_cast<float4 *>(p.part_o + at * D + d) = acc;
-            if (d == 0) p.part_ml[at] = make_float2(M, L);
+            uint32_t w[D / 8];
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (ok) u = *reinterpret_cast<const uint4 *>(row + q4 * (D / 4) + 8 * i);
+                w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+            }
+#pragma unroll
+            for (int s = 0; s < C::STEPS; ++s) {
+                if constexpr (BITS == 8) {
+                    qf[s][0] = w[2 * s], qf[s][1] = w[2 * s + 1];
+                } else {
+                    // words of eight channels: step 2 i even nibbles (0, 4), (2, 6), step 2 i + 1
+                    // odd ones (1, 5), (3, 7)
+                    const int i = 4 * (s / 2);
+                    const uint32_t sel = s % 2 ? 0x7632u : 0x5410u;
+                    qf[s][0] = pick(w[i], w[i + 2], sel), qf[s][1] = pick(w[i + 1], w[i + 3], sel);
+                }
+            }
         }
+    }
+    int tok[2];  // new token of rows 2 q4, 2 q4 + 1
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int r = rb * C::ROWS + 2 * q4 + e;
+        tok[e] = r < rows ? r / p.group : -1;
+    }
+
+    float o[C::MT][4];
+#pragma unroll
+    for (int i = 0; i < C::MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    int R = -100;
+
+    int stage = 0;
+    for (int t = t0 + warp; t < t1; t += TG) {
+        copy_wait<C::STAGES - 2>();
+        __syncwarp();
+        {
+            int free_stage = stage + C::STAGES - 1;
+            if (free_stage >= C::STAGES) free_stage -= C::STAGES;
+            if (next < t1) src.issue(next, free_stage, id);
+            copy_commit();
+            next += TG;
+            id = src.page_of(next);
+        }
+        const uint8_t *st = src.ring + stage * C::STAGE;
+        const uint32_t ka = smem_addr(st), va = ka + kTile * C::KS;
+        const uint8_t *tail = st + kTile * (C::KS + C::VS);
+        if (++stage == C::STAGES) stage = 0;
+
+        // ---- S^T: s[i][2 f + e] is token 16 i + 8 f + q8, row 2 q4 + e
+        float s[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] = 0.0f;
+            if constexpr (BITS == 16) {
+#pragma unroll
+                for (int k = 0; k < C::STEPS; ++k) {
+                    uint32_t f[4];
+                    load_matrix4(f, ka + (16 * i + (lane & 15)) * C::KS + (2 * k + (lane >> 4)) * 16);
+                    mma(s[i], f, qf[k][0], qf[k][1]);
+                }
+            } else {
+                constexpr int LB = C::RB / 4, UB = LB < 16 ? LB : 16;
+                const uint32_t at = ka + (16 * i + q8) * C::KS + q4 * LB;
+#pragma unroll
+                for (int u = 0; u < LB / UB; ++u) {
+                    uint32_t w[2][UB / 4];
+                    load_words<UB>(w[0], at + u * UB);
+                    load_words<UB>(w[1], at + 8 * C::KS + u * UB);
+#pragma unroll
+                    for (int k = 0; k < UB / 4; ++k) {
+                        if constexpr (BITS == 8) {
+                            const uint32_t x = w[0][k] ^ 0x80808080u, y = w[1][k] ^ 0x80808080u;
+                            const uint32_t f[4] = {pair8(x, false), pair8(y, false), pair8(x, true),
+                                                   pair8(y, true)};
+                            const int step = u * (UB / 4) + k;
+                            mma(s[i], f, qf[step][0], qf[step][1]);
+                        } else {
+                            const uint32_t x = w[0][k], y = w[1][k], x2 = x >> 8, y2 = y >> 8;
+                            const uint32_t f[4] = {pair4(x, false), pair4(y, false), pair4(x2, false),
+                                                   pair4(y2, false)};
+                            const uint32_t g[4] = {pair4(x, true), pair4(y, true), pair4(x2, true),
+                                                   pair4(y2, true)};
+                            const int step = 2 * (u * (UB / 4) + k);
+                            mma(s[i], f, qf[step][0], qf[step][1]);
+                            mma(s[i], g, qf[step + 1][0], qf[step + 1][1]);
+                        }
+                    }
+                }
+            }
+        }
+        // ---- scores in log2 units, unseen ones -infinity
+        float vsc[2][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                float ksc = p.scale_log2;
+                if constexpr (BITS != 16) {
+                    ksc *= *reinterpret_cast<const float *>(tail + 4 * (16 * i + 8 * f + q8));
+                    vsc[i][f] = *reinterpret_cast<const float *>(tail + 4 * (kTile + 16 * i + 8 * f + q8));
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) s[i][2 * f + e] *= ksc;
+            }
+        const unsigned live = *reinterpret_cast<const unsigned *>(tail + C::SCALES);
+        const int j0 = t * kTile - sq.ctx;
+        unsigned see[2] = {live, live};
+        const bool masked = live != 0xffffffffu || j0 + kTile > 0;
+        if (masked) {
+            see[0] &= seen(p, sq.first, tok[0], j0);
+            see[1] &= seen(p, sq.first, tok[1], j0);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (!((see[j & 1] >> (16 * i + 8 * (j >> 1) + q8)) & 1u)) s[i][j] = -INFINITY;
+        }
+        // ---- running maximum
+        float alpha[2], base[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float x = fmaxf(fmaxf(s[0][e], s[0][2 + e]), fmaxf(s[1][e], s[1][2 + e]));
+#pragma unroll
+            for (int y = 4; y < 32; y *= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, y));
+            x = fmaxf(x, m[e]);
+            base[e] = x == -INFINITY ? 0.0f : x;
+            alpha[e] = exp2_fast(m[e] - base[e]);
+            m[e] = x;
+            l[e] *= alpha[e];
+            base[e] -= kShift;
+        }
+        float unit = 1.0f;
+        if constexpr (BITS != 16) {
+            unsigned top = max(max(finite_bits(vsc[0][0]), finite_bits(vsc[0][1])),
+                               max(finite_bits(vsc[1][0]), finite_bits(vsc[1][1])));
+            top = __reduce_max_sync(0xffffffffu, top);
+            const int e = top_exponent(top);
+            if (e > R) {
+                const float f = exp2_fast(static_cast<float>(R - e));
+                alpha[0] *= f, alpha[1] *= f;
+                R = e;
+            }
+            unit = __uint_as_float(static_cast<unsigned>(127 - R) << 23);
+        }
+        if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
+#pragma unroll
+            for (int i = 0; i < C::MT; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[i][j] *= alpha[j & 1];
+        }
+        // ---- p, transposed into the second operand
+        uint32_t pf[2][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                float x[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    x[e] = exp2_fast(s[i][2 * f + e] - base[e]);
+                    l[e] += x[e];
+                    if constexpr (BITS != 16) {
+                        x[e] *= vsc[i][f] * unit;
+                        // an unseen token's scale may be anything
+                        if (masked && !((see[e] >> (16 * i + 8 * f + q8)) & 1u)) x[e] = 0.0f;
+                    }
+                }
+                pf[i][f] = transpose8(half2_of(x[0], x[1]));
+            }
+        // ---- O^T += V^T P^T
+        if constexpr (BITS == 16) {
+            // stored infinities and NaN in a tile that some row does not see
+            // whole: 0 * infinity would reach that row through the product
+            unsigned odd = 0;
+            if (masked) {
+                bool any = false;
+#pragma unroll
+                for (int c = 0; c < C::CPR; ++c) {
+                    uint32_t w[4];
+                    load_words<16>(w, va + lane * C::VS + 16 * c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        any |= (w[i] & 0x7c00u) == 0x7c00u || (w[i] & 0x7c000000u) == 0x7c000000u;
+                }
+                odd = __ballot_sync(0xffffffffu, any);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const unsigned o2 = odd >> (16 * i + 2 * q4);
+                const uint32_t keep0 = ~((o2 & 1u ? 0xffffu : 0u) | (o2 & 2u ? 0xffff0000u : 0u));
+                const uint32_t keep1 = ~((o2 & 256u ? 0xffffu : 0u) | (o2 & 512u ? 0xffff0000u : 0u));
+#pragma unroll
+                for (int c = 0; c < C::MT; ++c) {
+                    uint32_t f[4];
+                    load_matrix4_t(f, va + (16 * i + (lane & 7) + ((lane >> 4) & 1) * 8) * C::VS +
+                                          (2 * c + ((lane >> 3) & 1)) * 16);
+                    if (odd != 0) f[0] &= keep0, f[1] &= keep0, f[2] &= keep1, f[3] &= keep1;
+                    mma(o[c], f, pf[i][0], pf[i][1]);
+                }
+            }
+            // the tokens left out above, one by one, for the rows that see them
+            while (odd != 0) {
+                const int x = __ffs(odd) - 1;
+                odd &= odd - 1;
+                // lane 4 r + (x % 8) / 2 holds row r's p of this token
+                float pr[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    uint32_t w = 0;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int f = 0; f < 2; ++f) {
+                            const uint32_t y = __shfl_sync(0xffffffffu, pf[i][f], 4 * (2 * q4 + e) + (x % 8) / 2);
+                            if (x / 8 == 2 * i + f) w = y;
+                        }
+                    const __half2 h2 = *reinterpret_cast<const __half2 *>(&w);
+                    pr[e] = x % 2 ? __high2float(h2) : __low2float(h2);
+                }
+#pragma unroll
+                for (int c = 0; c < C::MT; ++c)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float v = __half2float(*reinterpret_cast<const __half *>(
+                            st + kTile * C::KS + x * C::VS + (16 * c + 8 * (j >> 1) + q8) * 2));
+                        if ((see[j & 1] >> x) & 1u) o[c][j] = fmaf(pr[j & 1], v, o[c][j]);
+                    }
+            }
+        } else {
+            // a lane's V operand is D / 8 consecutive channels of four tokens:
+            // rows q8 and q8 + 8 of tile c are channels 2 c and 2 c + 1 of them
+            constexpr int LB = C::RB / 8;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint32_t w[4][LB / 4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    load_words<LB>(w[x], va + (16 * i + 2 * q4 + (x & 1) + 8 * (x >> 1)) * C::VS + q8 * LB);
+#pragma unroll
+                for (int k = 0; k < LB / 4; ++k) {
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        if constexpr (BITS == 8) {
+                            const uint32_t sel = y ? 0x7362u : 0x5140u;
+                            const uint32_t a = pick(w[0][k], w[1][k], sel) ^ 0x80808080u;
+                            const uint32_t c = pick(w[2][k], w[3][k], sel) ^ 0x80808080u;
+                            const uint32_t f[4] = {pair8(a, false), pair8(a, true), pair8(c, false),
+                                                   pair8(c, true)};
+                            mma(o[2 * k + y], f, pf[i][0], pf[i][1]);
+                        } else {
+                            const uint32_t sel = y ? 0x7632u : 0x5410u;
+                            const uint32_t a = pick(w[0][k], w[1][k], sel), a2 = a >> 8;
+                            const uint32_t c = pick(w[2][k], w[3][k], sel), c2 = c >> 8;
+                            const uint32_t f[4] = {pair4(a, false), pair4(a, true), pair4(c, false),
+                                                   pair4(c, true)};
+                            const uint32_t g[4] = {pair4(a2, false), pair4(a2, true), pair4(c2, false),
+                                                   pair4(c2, true)};
+                            mma(o[4 * k + 2 * y], f, pf[i][0], pf[i][1]);
+                            mma(o[4 * k + 2 * y + 1], g, pf[i][0], pf[i][1]);
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    // ---- join the warps' results in shared memory (the ring is done with)
+    copy_wait<0>();
+    __syncthreads();
+    float *mo = reinterpret_cast<float *>(smem) + warp * C::ROWS * C::OP;
+    float2 *ml = reinterpret_cast<float2 *>(smem + C::NW * C::ROWS * C::OP * 4);
+    const float up = BITS == 16 ? 1.0f : __uint_as_float(static_cast<unsigned>(127 + R) << 23);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int y = 4; y < 32; y *= 2) l[e] += __shfl_xor_sync(0xffffffffu, l[e], y);
+        if (q8 == 0) ml[warp * C::ROWS + 2 * q4 + e] = make_float2(m[e], l[e]);
+#pragma unroll
+        for (int c = 0; c < C::MT; ++c)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int d = BITS == 16 ? 16 * c + 8 * x + q8 : q8 * (D / 8) + 2 * c + x;
+                mo[(2 * q4 + e) * C::OP + d] = o[c][2 * x + e] * up;
+            }
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < C::ROWS * (D / 4); x += C::NW * 32) {
+        const int r = x / (D / 4), d = x % (D / 4) * 4;
+        const int g = rb * C::ROWS + r;
+        if (g >= rows) break;
+        finish_row<C>(p, sq, smem, split, h, g, r, C::ROWS, TG, d);
     }
 }
 
@@ -671,19 +1078,20 @@ struct Plan {
     int wr, row_blocks, splits;
 };
 
-// Row warps: the fewest that hold the rows (a warp's products have 16), up to
-// four.  Splits of the cached tokens: enough CTAs for about two a resident
+// Up to eight rows: the transposed form (wr 0).  More: the fewest row warps
+// that hold the rows (a warp's products have 16), up to four.  Splits of the cached tokens: enough CTAs for about two a resident
 // slot, while each warp group keeps at least four tiles.
 Plan plan_of(const AttentionArgs &a) {
     Plan r;
     const int64_t rows = static_cast<int64_t>(a.max_tokens) * (a.q_heads / a.cache.heads);
-    r.wr = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-    r.row_blocks = static_cast<int>((rows + 16 * r.wr - 1) / (16 * r.wr));
+    r.wr = rows <= 8 ? 0 : rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+    const int block = r.wr == 0 ? 8 : 16 * r.wr;
+    r.row_blocks = static_cast<int>((rows + block - 1) / block);
     const int64_t items = static_cast<int64_t>(a.sequences) * a.cache.heads * r.row_blocks;
     const int64_t slots = static_cast<int64_t>(sm_count()) * 2;
     const int64_t tiles = (static_cast<int64_t>(a.max_context) + a.max_tokens + kTile - 1) / kTile;
     int64_t s = (2 * slots + items - 1) / items;
-    const int64_t most = tiles / (4 * (4 / r.wr));
+    const int64_t most = tiles / (4 * (4 / (r.wr == 0 ? 1 : r.wr)));
     s = s < most ? s : most;
     s = s < kMaxSplits ? s : kMaxSplits;
     r.splits = s < 1 ? 1 : static_cast<int>(s);
@@ -696,11 +1104,10 @@ size_t partial_bytes(const AttentionArgs &a, int splits) {
 }
 
 template <class C>
-quik_status run(const Params &p, cudaStream_t stream) {
-    if (!attribute_set_once(reinterpret_cast<const void *>(&tree_attention_kernel<C>), C::SMEM))
-        return QUIK_ERR_CUDA;
+quik_status run(const Params &p, void (*kernel)(Params), cudaStream_t stream) {
+    if (!attribute_set_once(reinterpret_cast<const void *>(kernel), C::SMEM)) return QUIK_ERR_CUDA;
     const dim3 grid(p.splits * p.row_blocks, p.heads, p.sequences);
-    tree_attention_kernel<C><<<grid, C::NW * 32, C::SMEM, stream>>>(p);
+    kernel<<<grid, C::NW * 32, C::SMEM, stream>>>(p);
     if (p.splits > 1) {
         const int64_t rows = static_cast<int64_t>(p.max_tokens) * p.group;
         tree_attention_join_kernel<C::D>
@@ -711,9 +1118,10 @@ quik_status run(const Params &p, cudaStream_t stream) {
 
 template <int BITS, int D>
 quik_status run_rows(const Params &p, int wr, cudaStream_t stream) {
-    if (wr == 1) return run<Cfg<BITS, D, 1, 4>>(p, stream);
-    if (wr == 2) return run<Cfg<BITS, D, 2, 4>>(p, stream);
-    return run<Cfg<BITS, D, 4, 4>>(p, stream);
+    if (wr == 0) return run<FewCfg<BITS, D>>(p, &tree_attention_few_kernel<FewCfg<BITS, D>>, stream);
+    if (wr == 1) return run<Cfg<BITS, D, 1, 4>>(p, &tree_attention_kernel<Cfg<BITS, D, 1, 4>>, stream);
+    if (wr == 2) return run<Cfg<BITS, D, 2, 4>>(p, &tree_attention_kernel<Cfg<BITS, D, 2, 4>>, stream);
+    return run<Cfg<BITS, D, 4, 4>>(p, &tree_attention_kernel<Cfg<BITS, D, 4, 4>>, stream);
 }
 
 template <int BITS>
