@@ -16,6 +16,7 @@
 // power of two 2^R above every scale met so far (O then is in units of 2^R), so
 // p stays within fp16 whatever the scales are.
 #include "quik_internal.h"
+#include "sm100.cuh"
 
 #include <cuda_fp16.h>
 
@@ -192,12 +193,13 @@ __device__ __forceinline__ Seq sequence(const Params &p, int b, bool report) {
 template <class C>
 struct Tiles {
     static constexpr int TH = 32 * C::WR;
-    const uint8_t *k, *v;
-    const float *ks, *vs;
+    const uint8_t *k, *v;   // this thread's place in the head's rows of page 0
+    const float *ks, *vs;   // this lane's scale there
     const int32_t *table;
     uint8_t *ring;
-    int page_shift, pages, heads, h, end, total;
-    int gt;  // thread among the TH
+    unsigned page_rows;     // rows of a page, all heads
+    int page_shift, pages, end, total;
+    int gt;                 // thread among the TH
     bool report;
 
     // Page of the half of the tile that this lane stands for (lanes 0-15, 16-31); -1: none.
@@ -205,46 +207,64 @@ struct Tiles {
         const int pos = tile * kTile + (threadIdx.x & 16);
         if (tile >= end || pos >= total) return -1;
         const int id = table[pos >> page_shift];
-        if (id >= 0 && id < pages) return id;
+        if (static_cast<unsigned>(id) < static_cast<unsigned>(pages)) return id;
         if (report && (threadIdx.x & 15) == 0) atomicAdd(&g_attn_bad_index, 1u);
         return -1;
     }
     // Start the copies of a tile (id: page_of of it).
     __device__ __forceinline__ void issue(int tile, int stage, int id) const {
         uint8_t *st = ring + stage * C::STAGE;
-        const uint32_t ka = smem_addr(st), va = ka + kTile * C::KS;
+        const int t = gt / C::CPR, c = gt % C::CPR;
+        const uint32_t ka = smem_addr(st) + t * C::KS + c * 16;
+        const uint32_t va = smem_addr(st) + kTile * C::KS + t * C::VS + c * 16;
         const int left = total - tile * kTile;  // tokens from the tile's first one on
-        int64_t row[2];
-        bool have[2];
+        const int p0 = __shfl_sync(0xffffffffu, id, 0), p1 = __shfl_sync(0xffffffffu, id, 16);
+        const int in_page = tile * kTile & ((1 << page_shift) - 1);
+        const int in_page1 = (tile * kTile + 16) & ((1 << page_shift) - 1);
+        // the row of the tile's first token; of its 16th from there, less 16: both
+        // halves then go by the token's number in the tile
+        const int64_t r0 = static_cast<int64_t>(static_cast<uint64_t>(static_cast<unsigned>(p0)) * page_rows) + in_page;
+        const int64_t r1 =
+            static_cast<int64_t>(static_cast<uint64_t>(static_cast<unsigned>(p1)) * page_rows) + (in_page1 - 16);
+        constexpr int N = kTile * C::CPR, HALF = N / 2, STEP = TH / C::CPR;  // STEP tokens a round
+        uint8_t *tail = st + kTile * (C::KS + C::VS);
+        if (left >= kTile && (p0 | p1) >= 0) {
+            const uint8_t *k0 = k + r0 * C::RB, *k1 = k + r1 * C::RB, *v0 = v + r0 * C::RB, *v1 = v + r1 * C::RB;
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
-            const int pid = __shfl_sync(0xffffffffu, id, 16 * f);
-            have[f] = pid >= 0;
-            row[f] = ((static_cast<int64_t>(have[f] ? pid : 0) * heads + h) << page_shift) +
-                     ((tile * kTile + 16 * f) & ((1 << page_shift) - 1));
-        }
-        constexpr int N = kTile * C::CPR, HALF = N / 2;
-#pragma unroll
-        for (int i = 0; i < (N + TH - 1) / TH; ++i) {
-            const int x = i * TH + gt, t = x / C::CPR, c = x % C::CPR;
-            if (N % TH != 0 && x >= N) break;
-            const bool second = HALF % TH == 0 ? i * TH >= HALF : x >= HALF;
-            const bool ok = (second ? have[1] : have[0]) && t < left;
-            // (x - HALF) * 16 = (t - 16) * RB + 16 c: the half's own offset
-            const int64_t off = (second ? row[1] * C::RB + (x - HALF) * 16 : row[0] * C::RB + x * 16);
-            copy16(ka + t * C::KS + c * 16, k + (ok ? off : 0), ok);
-            copy16(va + t * C::VS + c * 16, v + (ok ? off : 0), ok);
-        }
-        if (gt < 32) {
-            uint8_t *tail = st + kTile * (C::KS + C::VS);
-            const bool second = gt >= 16, ok = (second ? have[1] : have[0]) && gt < left;
-            if constexpr (C::BITS != 16) {
-                const int64_t r = second ? row[1] + (gt - 16) : row[0] + gt;
-                copy4(smem_addr(tail) + 4 * gt, ks + (ok ? r : 0), ok);
-                copy4(smem_addr(tail) + 4 * (kTile + gt), vs + (ok ? r : 0), ok);
+            for (int i = 0; i < (N + TH - 1) / TH; ++i) {
+                if (N % TH != 0 && gt >= N) break;
+                const bool second = HALF % TH == 0 ? i * TH >= HALF : gt >= HALF;
+                copy16(ka + i * STEP * C::KS, (second ? k1 : k0) + i * TH * 16, true);
+                copy16(va + i * STEP * C::VS, (second ? v1 : v0) + i * TH * 16, true);
             }
-            const unsigned live = __ballot_sync(0xffffffffu, ok);
-            if (gt == 0) *reinterpret_cast<unsigned *>(tail + C::SCALES) = live;
+            if (gt < 32) {
+                if constexpr (C::BITS != 16) {
+                    const int64_t r = gt >= 16 ? r1 : r0;
+                    copy4(smem_addr(tail) + 4 * gt, ks + r, true);
+                    copy4(smem_addr(tail) + 4 * (kTile + gt), vs + r, true);
+                }
+                if (gt == 0) *reinterpret_cast<unsigned *>(tail + C::SCALES) = 0xffffffffu;
+            }
+        } else {  // the last tile, or one with a bad page: zeros where there is nothing
+#pragma unroll
+            for (int i = 0; i < (N + TH - 1) / TH; ++i) {
+                if (N % TH != 0 && gt >= N) break;
+                const bool second = HALF % TH == 0 ? i * TH >= HALF : gt >= HALF;
+                const bool ok = (second ? p1 : p0) >= 0 && t + i * STEP < left;
+                const int64_t off = ok ? (second ? r1 : r0) * C::RB + i * TH * 16 : 0;
+                copy16(ka + i * STEP * C::KS, k + off, ok);
+                copy16(va + i * STEP * C::VS, v + off, ok);
+            }
+            if (gt < 32) {
+                const bool ok = (gt >= 16 ? p1 : p0) >= 0 && gt < left;
+                if constexpr (C::BITS != 16) {
+                    const int64_t r = ok ? (gt >= 16 ? r1 : r0) : 0;
+                    copy4(smem_addr(tail) + 4 * gt, ks + r, ok);
+                    copy4(smem_addr(tail) + 4 * (kTile + gt), vs + r, ok);
+                }
+                const unsigned live = __ballot_sync(0xffffffffu, ok);
+                if (gt == 0) *reinterpret_cast<unsigned *>(tail + C::SCALES) = live;
+            }
         }
     }
 };
@@ -253,10 +273,13 @@ template <class C>
 __device__ __forceinline__ Tiles<C> tiles_of(const Params &p, const Seq &sq, int b, int h, int end, uint8_t *ring,
                                              int gt, bool report) {
     Tiles<C> t;
-    t.k = p.k, t.v = p.v, t.ks = p.ks, t.vs = p.vs;
+    const int64_t head = static_cast<int64_t>(h) << p.page_shift;
+    t.k = p.k + head * C::RB + gt * 16, t.v = p.v + head * C::RB + gt * 16;
+    t.ks = p.ks + head + gt % 32, t.vs = p.vs + head + gt % 32;
     t.table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
     t.ring = ring;
-    t.page_shift = p.page_shift, t.pages = p.pages, t.heads = p.heads, t.h = h;
+    t.page_rows = static_cast<unsigned>(p.heads) << p.page_shift;
+    t.page_shift = p.page_shift, t.pages = p.pages;
     t.end = end, t.total = sq.total, t.gt = gt, t.report = report;
     return t;
 }
@@ -499,18 +522,21 @@ __global__ void __launch_bounds__(C::NW * 32) tree_attention_kernel(const Params
         // ---- the unit of the values' scales
         float unit = 1.0f;
         if constexpr (BITS != 16) {
-            unsigned top = 0;  // largest finite magnitude, by its bits
+            // only a scale above the unit (or one that is not finite) has a closer look
+            unit = __uint_as_float(static_cast<unsigned>(127 - R) << 23);
+            float big = 0.0f;
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
+            for (int n = 0; n < 4; ++n) big = fmaxf(fmaxf(big, fabsf(vsc[n][0])), fabsf(vsc[n][1]));
+            if (__any_sync(0xffffffffu, big * unit > 1.0f)) {
+                unsigned top = 0;  // largest finite magnitude, by its bits
 #pragma unroll
-                for (int e = 0; e < 2; ++e) top = max(top, finite_bits(vsc[n][e]));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int e = top_exponent(top);
-            if (e > R) {
-                const float f = exp2_fast(static_cast<float>(R - e));
-                alpha[0] *= f, alpha[1] *= f;
-                R = e;
+                for (int n = 0; n < 4; ++n) top = max(top, max(finite_bits(vsc[n][0]), finite_bits(vsc[n][1])));
+                const int e = top_exponent(__reduce_max_sync(0xffffffffu, top));
+                if (e > R) {
+                    const float f = exp2_fast(static_cast<float>(R - e));
+                    alpha[0] *= f, alpha[1] *= f;
+                    R = e;
+                }
             }
             unit = __uint_as_float(static_cast<unsigned>(127 - R) << 23);
         }
@@ -877,14 +903,19 @@ __global__ void __launch_bounds__(C::NW * 32, C::BITS == 4 ? 5 : 4) tree_attenti
         }
         float unit = 1.0f;
         if constexpr (BITS != 16) {
-            unsigned top = max(max(finite_bits(vsc[0][0]), finite_bits(vsc[0][1])),
-                               max(finite_bits(vsc[1][0]), finite_bits(vsc[1][1])));
-            top = __reduce_max_sync(0xffffffffu, top);
-            const int e = top_exponent(top);
-            if (e > R) {
-                const float f = exp2_fast(static_cast<float>(R - e));
-                alpha[0] *= f, alpha[1] *= f;
-                R = e;
+            // only a scale above the unit (or one that is not finite) has a closer look
+            unit = __uint_as_float(static_cast<unsigned>(127 - R) << 23);
+            const float big = fmaxf(fmaxf(fabsf(vsc[0][0]), fabsf(vsc[0][1])),
+                                    fmaxf(fabsf(vsc[1][0]), fabsf(vsc[1][1])));
+            if (__any_sync(0xffffffffu, big * unit > 1.0f)) {
+                const unsigned top = max(max(finite_bits(vsc[0][0]), finite_bits(vsc[0][1])),
+                                         max(finite_bits(vsc[1][0]), finite_bits(vsc[1][1])));
+                const int e = top_exponent(__reduce_max_sync(0xffffffffu, top));
+                if (e > R) {
+                    const float f = exp2_fast(static_cast<float>(R - e));
+                    alpha[0] *= f, alpha[1] *= f;
+                    R = e;
+                }
             }
             unit = __uint_as_float(static_cast<unsigned>(127 - R) << 23);
         }
@@ -1038,38 +1069,56 @@ __global__ void __launch_bounds__(C::NW * 32, C::BITS == 4 ? 5 : 4) tree_attenti
     }
 }
 
-// Join the splits' results: one warp a row.
+// Join the splits' results: a block of four warps a row, each warp every fourth
+// split, eight loads in flight.  (One warp a row, one split after the other:
+// 24 us for 64 splits.)
 template <int D>
 __global__ void __launch_bounds__(128) tree_attention_join_kernel(const Params p) {
-    const int lane = threadIdx.x % 32;
+    __shared__ float acc_s[4][D];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int h = blockIdx.y, b = blockIdx.z;
+    ptx::grid_dependency_wait();
     const Seq sq = sequence(p, b, false);
-    const int g = blockIdx.x * 4 + threadIdx.x / 32;
+    const int g = blockIdx.x;
     if (g >= sq.n * p.group) return;
     const int head = h * p.group + g % p.group, token = sq.first + g / p.group;
     const int64_t row = static_cast<int64_t>(token) * p.q_heads + head;
     const int64_t step = static_cast<int64_t>(p.tokens) * p.q_heads;
-    float M = -INFINITY;
-    for (int s = lane; s < p.splits; s += 32) M = fmaxf(M, p.part_ml[s * step + row].x);
+    // lanes hold the maxima and sums of up to 64 splits
+    const float2 none = make_float2(-INFINITY, 0.0f);
+    const float2 a0 = lane < p.splits ? p.part_ml[lane * step + row] : none;
+    const float2 a1 = lane + 32 < p.splits ? p.part_ml[(lane + 32) * step + row] : none;
+    float M = fmaxf(a0.x, a1.x);
 #pragma unroll
     for (int x = 1; x < 32; x *= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
     const float base = M == -INFINITY ? 0.0f : M;
+    const float f0 = exp2_fast(a0.x - base), f1 = exp2_fast(a1.x - base);
+    float L = fmaf(f0, a0.y, f1 * a1.y);
+#pragma unroll
+    for (int x = 1; x < 32; x *= 2) L += __shfl_xor_sync(0xffffffffu, L, x);
     constexpr int V = D / 32;
-    float L = 0.0f, acc[V] = {};
-    for (int s = 0; s < p.splits; ++s) {
-        const float2 a = p.part_ml[s * step + row];
-        const float f = exp2_fast(a.x - base);
-        L = fmaf(f, a.y, L);
+    float acc[V] = {};
+#pragma unroll 8
+    for (int s = warp; s < p.splits; s += 4) {
+        const float f = __shfl_sync(0xffffffffu, s < 32 ? f0 : f1, s % 32);
         const float *src = p.part_o + (s * step + row) * D + lane * V;
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] = fmaf(f, src[i], acc[i]);
     }
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-    uint16_t *dst = p.out + static_cast<int64_t>(token) * p.out_stride + head * D + lane * V;
 #pragma unroll
-    for (int i = 0; i < V; i += 2)
-        *reinterpret_cast<uint32_t *>(dst + i) = half2_of(acc[i] * inv, acc[i + 1] * inv);
-    if (lane == 0 && p.lse != nullptr)
+    for (int i = 0; i < V; ++i) acc_s[warp][lane * V + i] = acc[i];
+    __syncthreads();
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    if (threadIdx.x < D / 2) {
+        const int d = 2 * threadIdx.x;
+        float x[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            x[i] = ((acc_s[0][d + i] + acc_s[1][d + i]) + (acc_s[2][d + i] + acc_s[3][d + i])) * inv;
+        *reinterpret_cast<uint32_t *>(p.out + static_cast<int64_t>(token) * p.out_stride + head * D + d) =
+            half2_of(x[0], x[1]);
+    }
+    if (threadIdx.x == 0 && p.lse != nullptr)
         p.lse[row] = L == 0.0f ? -INFINITY : (M - kShift + log2f(L)) * 0.693147180559945f;
 }
 
@@ -1109,9 +1158,17 @@ quik_status run(const Params &p, void (*kernel)(Params), cudaStream_t stream) {
     const dim3 grid(p.splits * p.row_blocks, p.heads, p.sequences);
     kernel<<<grid, C::NW * 32, C::SMEM, stream>>>(p);
     if (p.splits > 1) {
-        const int64_t rows = static_cast<int64_t>(p.max_tokens) * p.group;
-        tree_attention_join_kernel<C::D>
-            <<<dim3(static_cast<unsigned>((rows + 3) / 4), p.heads, p.sequences), 128, 0, stream>>>(p);
+        // launched while the first kernel runs; it waits for that kernel's results
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(static_cast<unsigned>(p.max_tokens) * p.group, p.heads, p.sequences);
+        cfg.blockDim = dim3(128);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, &tree_attention_join_kernel<C::D>, p) != cudaSuccess) return QUIK_ERR_CUDA;
     }
     return cudaGetLastError() == cudaSuccess ? QUIK_OK : QUIK_ERR_CUDA;
 }
