@@ -47,6 +47,11 @@ struct Params {
     float *lse;
     float *part_o;   // [splits][tokens * q_heads][D]
     float2 *part_ml; // [splits][tokens * q_heads]
+    // up to 8 rows: pieces (workers + items of them), each 8 rows as the warps hold them
+    int workers;
+    float4 *piece_o;   // [pieces][D / 16][32]
+    float2 *piece_ml;  // [pieces][8]
+    int *item_span;    // [items][2]: the workers that hold an item's first and last tile
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
@@ -135,7 +140,9 @@ __device__ __forceinline__ uint32_t pair8(uint32_t x, bool hi) {
 // the nibbles at bits 0 and 16 (up: 4 and 20) of x as a pair
 __device__ __forceinline__ uint32_t pair4(uint32_t x, bool up) {
     const uint32_t c = up ? 0x54805480u : 0x64086408u;  // 64 + 8, 1024 + 8
-    return half2_sub((x & (up ? 0x00f000f0u : 0x000f000fu)) ^ c, c);
+    uint32_t r;  // (x & mask) ^ c
+    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(x), "r"(up ? 0x00f000f0u : 0x000f000fu), "r"(c));
+    return half2_sub(r, c);
 }
 
 // WR warps share a tile, 16 rows each; NW / WR such groups take tiles in turn.
@@ -701,19 +708,29 @@ __global__ void __launch_bounds__(C::NW * 32) tree_attention_kernel(const Params
 // query rows as its 8 columns, a decoding step's few rows cost half the
 // products, accumulators and exponentials.  P^T turns from the accumulators'
 // layout into the second product's operand by movmatrix.
+//
+// The work, tiles of all sequences, key heads and blocks of 8 rows one after
+// the other, is cut into equal runs, one a warp, whatever the sequences'
+// lengths: no warp waits for another, and all end together.  A run crosses
+// from one item (sequence, key head, row block) to the next without emptying
+// its ring.  What a warp finds for an item is a piece; a second kernel joins an
+// item's pieces.  Piece number = worker + item: along the runs one or the other
+// goes up at every step, so no two pieces share a number.  (CTAs of four warps
+// on 1 / 2 of an item each, joined in shared memory: 44.5 us for 16 sequences
+// over INT4, of which 28 us remained without any arithmetic.)
 template <int BITS_, int D_>
 struct FewCfg {
-    static constexpr int BITS = BITS_, D = D_, WR = 1, NW = 4, TG = 4, ROWS = 8;
+    static constexpr int BITS = BITS_, D = D_, WR = 1, NW = 4, ROWS = 8;
     static constexpr int RB = D * BITS / 8, CPR = RB / 16;
     static constexpr int KS = RB >= 128 ? RB + 16 : RB, VS = RB + 16;
     static constexpr int SCALES = BITS == 16 ? 0 : 2 * kTile * 4;
-    static constexpr int STAGE = kTile * (KS + VS) + SCALES + 16;
+    static constexpr int STAGE = kTile * (KS + VS) + SCALES + 32;
     static constexpr int STAGES = STAGE > 4000 && STAGE < 6000 ? 2 : 3;
-    static constexpr int RING = TG * STAGES * STAGE;
-    static constexpr int OP = D + 4;
-    static constexpr int MERGE = NW * ROWS * OP * 4 + NW * ROWS * 8;
-    static constexpr int SMEM = RING > MERGE ? RING : MERGE;
+    static constexpr int SMEM = NW * STAGES * STAGE;
     static constexpr int STEPS = D / 16, MT = D / 16;
+    // resident CTAs of an SM: by 228 KB of shared memory and 65536 registers
+    static constexpr int BY_SMEM = 233472 / (SMEM + 1024);
+    static constexpr int CTAS = BY_SMEM < 4 ? BY_SMEM : 4;
 };
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -721,101 +738,202 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
+// Tiles of an item of sequence b, and its items.
+struct Load {
+    int tiles, items;
+};
+__device__ __forceinline__ Load load_of(const Params &p, const Seq &s) {
+    Load l;
+    l.tiles = (s.total + kTile - 1) / kTile;
+    l.items = s.n == 0 ? 0 : p.heads * ((s.n * p.group + 7) / 8);
+    return l;
+}
+
+// Sum of the tiles of sequences [0, n) (whole warp; every lane gets it).
+__device__ __forceinline__ int64_t tiles_before(const Params &p, int n, bool report) {
+    int64_t sum = 0;
+    for (int b = threadIdx.x % 32; b < n; b += 32) {
+        const Load l = load_of(p, sequence(p, b, report));
+        sum += static_cast<int64_t>(l.tiles) * l.items;
+    }
+#pragma unroll
+    for (int x = 1; x < 32; x *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    return sum;
+}
+
+// A place in the work: an item of sequence b and a tile of it.
+struct Cursor {
+    int b, item, tile, tiles, items;
+    Seq sq;
+};
+// The next sequence that has any work, from b on.
+__device__ __forceinline__ void enter(const Params &p, Cursor &c, int b) {
+    for (; b < p.sequences; ++b) {
+        c.sq = sequence(p, b, false);
+        const Load l = load_of(p, c.sq);
+        c.b = b, c.tiles = l.tiles, c.items = l.items;
+        if (l.tiles > 0 && l.items > 0) return;
+    }
+}
+
 template <class C>
-__global__ void __launch_bounds__(C::NW * 32, C::BITS == 4 ? 5 : 4) tree_attention_few_kernel(const Params p) {
-    constexpr int BITS = C::BITS, D = C::D, TG = C::TG;
+__global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel(const Params p) {
+    constexpr int BITS = C::BITS, D = C::D;
     extern __shared__ __align__(16) uint8_t smem[];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const int split = blockIdx.x % p.splits, rb = blockIdx.x / p.splits;
-    const int h = blockIdx.y, b = blockIdx.z;
-    const Seq sq = sequence(p, b, blockIdx.x == 0 && h == 0 && threadIdx.x == 0);
-    const int rows = sq.n * p.group;
-    if (rb * C::ROWS >= rows) return;
-    const int tiles = (sq.total + kTile - 1) / kTile;
-    const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * split / p.splits);
-    const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / p.splits);
+    const int worker = blockIdx.x * C::NW + warp;
 
-    const Tiles<C> src = tiles_of<C>(p, sq, b, h, t1, smem + warp * C::STAGES * C::STAGE, lane, rb == 0);
-    int next = t0 + warp;
-    int id = src.page_of(next);
+    // ---- this worker's run
+    const int64_t all = tiles_before(p, p.sequences, blockIdx.x == 0 && warp == 0);
+    // no more workers than tiles: every worker between an item's first and last has a piece of it
+    const int64_t workers = all < p.workers ? all : p.workers;
+    if (worker >= workers) return;
+    const int64_t from = all * worker / workers;
+    int left = static_cast<int>(all * (worker + 1) / workers - from);  // tiles still to be issued
+    Cursor at;
+    at.item = 0, at.tile = 0;
+    {
+        int64_t before = 0;
+        for (int b0 = 0; b0 < p.sequences; b0 += 32) {
+            int64_t mine = 0;
+            if (b0 + lane < p.sequences) {
+                const Load l = load_of(p, sequence(p, b0 + lane, false));
+                mine = static_cast<int64_t>(l.tiles) * l.items;
+            }
+            int64_t to = mine;  // tiles up to and with this lane's sequence
+#pragma unroll
+            for (int x = 1; x < 32; x *= 2) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, to, x);
+                if (lane >= x) to += y;
+            }
+            to += before;
+            const unsigned past = __ballot_sync(0xffffffffu, to > from);
+            if (past != 0) {
+                const int src = __ffs(past) - 1;
+                const int64_t begin = __shfl_sync(0xffffffffu, to - mine, src);
+                enter(p, at, b0 + src);
+                at.item = static_cast<int>((from - begin) / at.tiles);
+                at.tile = static_cast<int>((from - begin) % at.tiles);
+                break;
+            }
+            before = __shfl_sync(0xffffffffu, to, 31);
+        }
+    }
+    int todo = left;
+
+    uint8_t *ring = smem + warp * C::STAGES * C::STAGE;
+    // of the place to be issued next: its rows, its page number
+    Tiles<C> src;
+    int id;
+    auto locate = [&]() {
+        const int blocks = at.items / p.heads;
+        src = tiles_of<C>(p, at.sq, at.b, at.item / blocks, at.tiles, ring, lane, at.item % blocks == 0);
+    };
+    locate();
+    id = src.page_of(at.tile);
+    // copies of the next tile, what the products need to know of it, and one step on
+    bool start = true;
+    auto issue = [&](int stage) {
+        if (left == 0) return;
+        src.issue(at.tile, stage, id);
+        const bool last = left == 1 || at.tile + 1 == at.tiles;
+        if (lane == 0) {
+            // beside `live`: first new token of the tile, item, sequence, and whether
+            // the tile is the first or last of a piece, the first or last of its item
+            uint8_t *tail = ring + stage * C::STAGE + kTile * (C::KS + C::VS) + C::SCALES;
+            *reinterpret_cast<int4 *>(tail + 16) =
+                make_int4(at.tile * kTile - at.sq.ctx, at.item, at.b,
+                          (start ? 1 : 0) | (last ? 2 : 0) | (at.tile == 0 ? 4 : 0) |
+                              (at.tile + 1 == at.tiles ? 8 : 0));
+        }
+        start = last;
+        if (--left == 0) return;
+        if (++at.tile == at.tiles) {
+            at.tile = 0;
+            if (++at.item == at.items) {
+                at.item = 0;
+                enter(p, at, at.b + 1);
+            }
+            locate();
+        }
+        id = src.page_of(at.tile);
+    };
 #pragma unroll
     for (int s = 0; s < C::STAGES - 1; ++s) {
-        if (next < t1) src.issue(next, s, id);
+        issue(s);
         copy_commit();
-        next += TG;
-        id = src.page_of(next);
     }
 
-    // ---- the query rows as the products' second operand: this lane's is row
-    // q8, and of it the channels that the lanes' K words give up together
     const int q4 = lane & 3, q8 = lane >> 2;
-    uint32_t qf[C::STEPS][2];
-    {
-        const int r = rb * C::ROWS + q8;
-        const bool ok = r < rows;
-        const uint16_t *row = p.q;
-        if (ok)
-            row += static_cast<int64_t>(sq.first + r / p.group) * p.q_stride +
-                   static_cast<int64_t>(h * p.group + r % p.group) * D;
-        if constexpr (BITS == 16) {
-#pragma unroll
-            for (int s = 0; s < C::STEPS; ++s)
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    qf[s][x] = ok ? *reinterpret_cast<const uint32_t *>(row + 16 * s + 8 * x + 2 * q4) : 0u;
-        } else {
-            uint32_t w[D / 8];
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                uint4 u = make_uint4(0, 0, 0, 0);
-                if (ok) u = *reinterpret_cast<const uint4 *>(row + q4 * (D / 4) + 8 * i);
-                w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
-            }
-#pragma unroll
-            for (int s = 0; s < C::STEPS; ++s) {
-                if constexpr (BITS == 8) {
-                    qf[s][0] = w[2 * s], qf[s][1] = w[2 * s + 1];
-                } else {
-                    // words of eight channels: step 2 i even nibbles (0, 4), (2, 6), step 2 i + 1
-                    // odd ones (1, 5), (3, 7)
-                    const int i = 4 * (s / 2);
-                    const uint32_t sel = s % 2 ? 0x7632u : 0x5410u;
-                    qf[s][0] = pick(w[i], w[i + 2], sel), qf[s][1] = pick(w[i + 1], w[i + 3], sel);
-                }
-            }
-        }
-    }
-    int tok[2];  // new token of rows 2 q4, 2 q4 + 1
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int r = rb * C::ROWS + 2 * q4 + e;
-        tok[e] = r < rows ? r / p.group : -1;
-    }
-
-    float o[C::MT][4];
-#pragma unroll
-    for (int i = 0; i < C::MT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-    int R = -100;
+    uint32_t qf[C::STEPS][2];  // the query rows as the products' second operand
+    int tok[2], first = 0;     // new token of rows 2 q4, 2 q4 + 1; the sequence's first row
+    float o[C::MT][4], m[2], l[2];
+    int R = 0;
 
     int stage = 0;
-    for (int t = t0 + warp; t < t1; t += TG) {
+    for (; todo > 0; --todo) {
         copy_wait<C::STAGES - 2>();
         __syncwarp();
-        {
-            int free_stage = stage + C::STAGES - 1;
-            if (free_stage >= C::STAGES) free_stage -= C::STAGES;
-            if (next < t1) src.issue(next, free_stage, id);
-            copy_commit();
-            next += TG;
-            id = src.page_of(next);
-        }
-        const uint8_t *st = src.ring + stage * C::STAGE;
+        issue(stage + C::STAGES - 1 >= C::STAGES ? stage - 1 : stage + C::STAGES - 1);
+        copy_commit();
+        const uint8_t *st = ring + stage * C::STAGE;
         const uint32_t ka = smem_addr(st), va = ka + kTile * C::KS;
         const uint8_t *tail = st + kTile * (C::KS + C::VS);
         if (++stage == C::STAGES) stage = 0;
+        const unsigned live = *reinterpret_cast<const unsigned *>(tail + C::SCALES);
+        const int4 place = *reinterpret_cast<const int4 *>(tail + C::SCALES + 16);
+        const int j0 = place.x;
+        if (place.w & 1) {
+            // ---- a new item: this lane's query row is q8, and of it the channels
+            // that the lanes' K words give up together
+            first = p.cu[place.z];
+            const int rows = (p.cu[place.z + 1] - first) * p.group, blocks = (rows + 7) / 8;
+            const int h = place.y / blocks, r0 = place.y % blocks * 8;
+            const int r = r0 + q8;
+            const bool ok = r < rows;
+            const uint16_t *row = p.q;
+            if (ok)
+                row += static_cast<int64_t>(first + r / p.group) * p.q_stride +
+                       static_cast<int64_t>(h * p.group + r % p.group) * D;
+            if constexpr (BITS == 16) {
+#pragma unroll
+                for (int s = 0; s < C::STEPS; ++s)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        qf[s][x] = ok ? *reinterpret_cast<const uint32_t *>(row + 16 * s + 8 * x + 2 * q4) : 0u;
+            } else {
+                uint32_t w[D / 8];
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    uint4 u = make_uint4(0, 0, 0, 0);
+                    if (ok) u = *reinterpret_cast<const uint4 *>(row + q4 * (D / 4) + 8 * i);
+                    w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+                }
+#pragma unroll
+                for (int s = 0; s < C::STEPS; ++s) {
+                    if constexpr (BITS == 8) {
+                        qf[s][0] = w[2 * s], qf[s][1] = w[2 * s + 1];
+                    } else {
+                        // words of eight channels: step 2 i even nibbles (0, 4), (2, 6), step 2 i + 1
+                        // odd ones (1, 5), (3, 7)
+                        const int i = 4 * (s / 2);
+                        const uint32_t sel = s % 2 ? 0x7632u : 0x5410u;
+                        qf[s][0] = pick(w[i], w[i + 2], sel), qf[s][1] = pick(w[i + 1], w[i + 3], sel);
+                    }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int x = r0 + 2 * q4 + e;
+                tok[e] = x < rows ? x / p.group : -1;
+                m[e] = -INFINITY, l[e] = 0.0f;
+            }
+            R = -100;
+#pragma unroll
+            for (int i = 0; i < C::MT; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
+        }
 
         // ---- S^T: s[i][2 f + e] is token 16 i + 8 f + q8, row 2 q4 + e
         float s[2][4];
@@ -874,13 +992,11 @@ __global__ void __launch_bounds__(C::NW * 32, C::BITS == 4 ? 5 : 4) tree_attenti
 #pragma unroll
                 for (int e = 0; e < 2; ++e) s[i][2 * f + e] *= ksc;
             }
-        const unsigned live = *reinterpret_cast<const unsigned *>(tail + C::SCALES);
-        const int j0 = t * kTile - sq.ctx;
         unsigned see[2] = {live, live};
         const bool masked = live != 0xffffffffu || j0 + kTile > 0;
         if (masked) {
-            see[0] &= seen(p, sq.first, tok[0], j0);
-            see[1] &= seen(p, sq.first, tok[1], j0);
+            see[0] &= seen(p, first, tok[0], j0);
+            see[1] &= seen(p, first, tok[1], j0);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -1039,34 +1155,95 @@ __global__ void __launch_bounds__(C::NW * 32, C::BITS == 4 ? 5 : 4) tree_attenti
                 }
             }
         }
-    }
-
-    // ---- join the warps' results in shared memory (the ring is done with)
-    copy_wait<0>();
-    __syncthreads();
-    float *mo = reinterpret_cast<float *>(smem) + warp * C::ROWS * C::OP;
-    float2 *ml = reinterpret_cast<float2 *>(smem + C::NW * C::ROWS * C::OP * 4);
-    const float up = BITS == 16 ? 1.0f : __uint_as_float(static_cast<unsigned>(127 + R) << 23);
+        if (place.w & 12) {
+            const int64_t blocks = (p.max_tokens * static_cast<int64_t>(p.group) + 7) / 8;
+            int *span = p.item_span + 2 * (place.z * (p.heads * blocks) + place.y);
+            if (lane == 0 && (place.w & 4)) span[0] = worker;
+            if (lane == 0 && (place.w & 8)) span[1] = worker;
+        }
+        if (place.w & 2) {
+            // ---- the piece, as the lanes hold it; rows that do not exist are left out
+            const int64_t blocks = (p.max_tokens * static_cast<int64_t>(p.group) + 7) / 8;
+            const int64_t item = place.z * (p.heads * blocks) + place.y, piece = worker + item;
+            const float up = BITS == 16 ? 1.0f : __uint_as_float(static_cast<unsigned>(127 + R) << 23);
+            float4 *dst = p.piece_o + piece * (C::MT * 32) + lane;
+            if (tok[0] >= 0) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int y = 4; y < 32; y *= 2) l[e] += __shfl_xor_sync(0xffffffffu, l[e], y);
-        if (q8 == 0) ml[warp * C::ROWS + 2 * q4 + e] = make_float2(m[e], l[e]);
-#pragma unroll
-        for (int c = 0; c < C::MT; ++c)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int d = BITS == 16 ? 16 * c + 8 * x + q8 : q8 * (D / 8) + 2 * c + x;
-                mo[(2 * q4 + e) * C::OP + d] = o[c][2 * x + e] * up;
+                for (int c = 0; c < C::MT; ++c)
+                    dst[c * 32] = make_float4(o[c][0] * up, o[c][1] * up, o[c][2] * up, o[c][3] * up);
             }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float sum = l[e];
+#pragma unroll
+                for (int y = 4; y < 32; y *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, y);
+                if (q8 == 0) p.piece_ml[piece * 8 + 2 * q4 + e] = make_float2(m[e], sum);
+            }
+        }
     }
+}
+
+// Join an item's pieces: a block of 4 D threads a row, thread (k, d) every
+// fourth piece's channel d.
+template <class C>
+__global__ void __launch_bounds__(4 * C::D) tree_attention_few_join_kernel(const Params p) {
+    constexpr int D = C::D;
+    __shared__ float acc_s[4][D], sum_s[4], max_s[4 * D / 32];
+    const int h = blockIdx.y, b = blockIdx.z, g = blockIdx.x;
+    ptx::grid_dependency_wait();
+    const Seq sq = sequence(p, b, false);
+    if (g >= sq.n * p.group) return;
+    const Load ld = load_of(p, sq);
+    const int r = g % 8, item = h * (ld.items / p.heads) + g / 8;
+    const int64_t blocks = (p.max_tokens * static_cast<int64_t>(p.group) + 7) / 8;
+    const int64_t index = b * (p.heads * blocks) + item;
+    int w0 = 0, count = 0;
+    if (ld.tiles > 0) {
+        w0 = p.item_span[2 * index];
+        count = p.item_span[2 * index + 1] - w0 + 1;
+    }
+    const int64_t piece0 = index + w0;
+    float M = -INFINITY;
+    for (int s = threadIdx.x; s < count; s += 4 * D) M = fmaxf(M, p.piece_ml[(piece0 + s) * 8 + r].x);
+#pragma unroll
+    for (int x = 1; x < 32; x *= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    if (threadIdx.x % 32 == 0) max_s[threadIdx.x / 32] = M;
     __syncthreads();
-    for (int x = threadIdx.x; x < C::ROWS * (D / 4); x += C::NW * 32) {
-        const int r = x / (D / 4), d = x % (D / 4) * 4;
-        const int g = rb * C::ROWS + r;
-        if (g >= rows) break;
-        finish_row<C>(p, sq, smem, split, h, g, r, C::ROWS, TG, d);
+#pragma unroll
+    for (int x = 0; x < 4 * D / 32; ++x) M = fmaxf(M, max_s[x]);
+    const float base = M == -INFINITY ? 0.0f : M;
+    // where the lanes hold channel d of row r
+    const int k = threadIdx.x / D, d = threadIdx.x % D;
+    const int q8 = C::BITS == 16 ? d % 8 : d / (D / 8);
+    const int c = C::BITS == 16 ? d / 16 : d % (D / 8) / 2, x = C::BITS == 16 ? d / 8 % 2 : d % 2;
+    const float *src = reinterpret_cast<const float *>(p.piece_o) +
+                       ((piece0 * C::MT + c) * 32 + q8 * 4 + r / 2) * 4 + 2 * x + r % 2;
+    float acc = 0.0f, L = 0.0f;
+#pragma unroll 8
+    for (int s = k; s < count; s += 4) {
+        const float2 a = p.piece_ml[(piece0 + s) * 8 + r];
+        const float f = exp2_fast(a.x - base);
+        acc = fmaf(f, src[static_cast<int64_t>(s) * (C::MT * 128)], acc);
+        L = fmaf(f, a.y, L);
     }
+    acc_s[k][d] = acc;
+    if (d == 0) sum_s[k] = L;
+    __syncthreads();
+    L = (sum_s[0] + sum_s[1]) + (sum_s[2] + sum_s[3]);
+    const int head = h * p.group + g % p.group, token = sq.first + g / p.group;
+    if (threadIdx.x < D / 2) {
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+        const int e = 2 * threadIdx.x;
+        float y[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            y[i] = ((acc_s[0][e + i] + acc_s[1][e + i]) + (acc_s[2][e + i] + acc_s[3][e + i])) * inv;
+        *reinterpret_cast<uint32_t *>(p.out + static_cast<int64_t>(token) * p.out_stride + head * D + e) =
+            half2_of(y[0], y[1]);
+    }
+    if (threadIdx.x == 0 && p.lse != nullptr)
+        p.lse[static_cast<int64_t>(token) * p.q_heads + head] =
+            L == 0.0f ? -INFINITY : (M - kShift + log2f(L)) * 0.693147180559945f;
 }
 
 // Join the splits' results: a block of four warps a row, each warp every fourth
@@ -1125,31 +1302,76 @@ __global__ void __launch_bounds__(128) tree_attention_join_kernel(const Params p
 // ------------------------------------------------------------------ host side
 struct Plan {
     int wr, row_blocks, splits;
+    int workers;      // up to 8 rows: warps that share the tiles
+    int64_t pieces;
 };
 
-// Up to eight rows: the transposed form (wr 0).  More: the fewest row warps
-// that hold the rows (a warp's products have 16), up to four.  Splits of the cached tokens: enough CTAs for about two a resident
-// slot, while each warp group keeps at least four tiles.
+template <int BITS>
+int few_ctas(int head_dim) {
+    return head_dim == 64 ? FewCfg<BITS, 64>::CTAS : FewCfg<BITS, 128>::CTAS;
+}
+
+// Up to eight rows: the transposed form (wr 0), with as many workers as are
+// resident at once, but four tiles or more each where the hint is right.
+// More rows: the fewest row warps that hold them (a warp's products have 16),
+// up to four, and splits of the cached tokens, enough CTAs for about two a
+// resident slot, while each warp group keeps at least four tiles.
 Plan plan_of(const AttentionArgs &a) {
-    Plan r;
+    Plan r{};
     const int64_t rows = static_cast<int64_t>(a.max_tokens) * (a.q_heads / a.cache.heads);
     r.wr = rows <= 8 ? 0 : rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
     const int block = r.wr == 0 ? 8 : 16 * r.wr;
     r.row_blocks = static_cast<int>((rows + block - 1) / block);
     const int64_t items = static_cast<int64_t>(a.sequences) * a.cache.heads * r.row_blocks;
-    const int64_t slots = static_cast<int64_t>(sm_count()) * 2;
     const int64_t tiles = (static_cast<int64_t>(a.max_context) + a.max_tokens + kTile - 1) / kTile;
+    if (r.wr == 0) {
+        const int ctas = a.cache.kv_type == QUIK_KV_INT4   ? few_ctas<4>(a.cache.head_dim)
+                         : a.cache.kv_type == QUIK_KV_INT8 ? few_ctas<8>(a.cache.head_dim)
+                                                           : few_ctas<16>(a.cache.head_dim);
+        const int64_t want = (items * tiles + 15) / 16, most = static_cast<int64_t>(sm_count()) * ctas;
+        r.workers = 4 * static_cast<int>(want < 1 ? 1 : want < most ? want : most);
+        r.pieces = items + r.workers;
+        return r;
+    }
+    const int64_t slots = static_cast<int64_t>(sm_count()) * 2;
     int64_t s = (2 * slots + items - 1) / items;
-    const int64_t most = tiles / (4 * (4 / (r.wr == 0 ? 1 : r.wr)));
+    const int64_t most = tiles / (4 * (4 / r.wr));
     s = s < most ? s : most;
     s = s < kMaxSplits ? s : kMaxSplits;
     r.splits = s < 1 ? 1 : static_cast<int>(s);
     return r;
 }
 
-size_t partial_bytes(const AttentionArgs &a, int splits) {
-    if (splits == 1) return 0;
-    return static_cast<size_t>(splits) * a.tokens * a.q_heads * (a.cache.head_dim * 4 + 8);
+size_t partial_bytes(const AttentionArgs &a, const Plan &r) {
+    if (r.wr == 0)
+        return static_cast<size_t>(r.pieces) * 8 * (a.cache.head_dim * 4 + 8) +
+               static_cast<size_t>(r.pieces - r.workers) * 8;
+    if (r.splits == 1) return 0;
+    return static_cast<size_t>(r.splits) * a.tokens * a.q_heads * (a.cache.head_dim * 4 + 8);
+}
+
+// The join of a call's partial results, launched while the first kernel runs;
+// it waits for that kernel's results.
+quik_status launch_join(const Params &p, void (*kernel)(Params), int threads, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.max_tokens) * p.group, p.heads, p.sequences);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? QUIK_OK : QUIK_ERR_CUDA;
+}
+
+template <class C>
+quik_status run_few(const Params &p, cudaStream_t stream) {
+    void (*kernel)(Params) = &tree_attention_few_kernel<C>;
+    if (!attribute_set_once(reinterpret_cast<const void *>(kernel), C::SMEM)) return QUIK_ERR_CUDA;
+    kernel<<<p.workers / C::NW, C::NW * 32, C::SMEM, stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return QUIK_ERR_CUDA;
+    return launch_join(p, &tree_attention_few_join_kernel<C>, 4 * C::D, stream);
 }
 
 template <class C>
@@ -1158,24 +1380,15 @@ quik_status run(const Params &p, void (*kernel)(Params), cudaStream_t stream) {
     const dim3 grid(p.splits * p.row_blocks, p.heads, p.sequences);
     kernel<<<grid, C::NW * 32, C::SMEM, stream>>>(p);
     if (p.splits > 1) {
-        // launched while the first kernel runs; it waits for that kernel's results
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(static_cast<unsigned>(p.max_tokens) * p.group, p.heads, p.sequences);
-        cfg.blockDim = dim3(128);
-        cfg.stream = stream;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaLaunchKernelEx(&cfg, &tree_attention_join_kernel<C::D>, p) != cudaSuccess) return QUIK_ERR_CUDA;
+        const quik_status st = launch_join(p, &tree_attention_join_kernel<C::D>, 128, stream);
+        if (st != QUIK_OK) return st;
     }
     return cudaGetLastError() == cudaSuccess ? QUIK_OK : QUIK_ERR_CUDA;
 }
 
 template <int BITS, int D>
 quik_status run_rows(const Params &p, int wr, cudaStream_t stream) {
-    if (wr == 0) return run<FewCfg<BITS, D>>(p, &tree_attention_few_kernel<FewCfg<BITS, D>>, stream);
+    if (wr == 0) return run_few<FewCfg<BITS, D>>(p, stream);
     if (wr == 1) return run<Cfg<BITS, D, 1, 4>>(p, &tree_attention_kernel<Cfg<BITS, D, 1, 4>>, stream);
     if (wr == 2) return run<Cfg<BITS, D, 2, 4>>(p, &tree_attention_kernel<Cfg<BITS, D, 2, 4>>, stream);
     return run<Cfg<BITS, D, 4, 4>>(p, &tree_attention_kernel<Cfg<BITS, D, 4, 4>>, stream);
@@ -1188,7 +1401,7 @@ quik_status run_dim(const Params &p, int head_dim, int wr, cudaStream_t stream) 
 
 }  // namespace
 
-size_t attention_workspace(const AttentionArgs &a) { return partial_bytes(a, plan_of(a).splits); }
+size_t attention_workspace(const AttentionArgs &a) { return partial_bytes(a, plan_of(a)); }
 
 quik_status launch_tree_attention(const AttentionArgs &a, cudaStream_t stream) {
     const Plan plan = plan_of(a);
@@ -1223,6 +1436,10 @@ quik_status launch_tree_attention(const AttentionArgs &a, cudaStream_t stream) {
     p.part_o = a.partial;
     p.part_ml = reinterpret_cast<float2 *>(
         a.partial + static_cast<size_t>(plan.splits) * a.tokens * a.q_heads * a.cache.head_dim);
+    p.workers = plan.workers;
+    p.piece_o = reinterpret_cast<float4 *>(a.partial);
+    p.piece_ml = reinterpret_cast<float2 *>(a.partial + static_cast<size_t>(plan.pieces) * 8 * a.cache.head_dim);
+    p.item_span = reinterpret_cast<int *>(p.piece_ml + plan.pieces * 8);
     if (a.cache.kv_type == QUIK_KV_INT4) return run_dim<4>(p, a.cache.head_dim, plan.wr, stream);
     if (a.cache.kv_type == QUIK_KV_INT8) return run_dim<8>(p, a.cache.head_dim, plan.wr, stream);
     return run_dim<16>(p, a.cache.head_dim, plan.wr, stream);

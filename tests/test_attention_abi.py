@@ -130,14 +130,14 @@ def test_tree_attention_refusals(L):
 
 
 def test_attention_workspace(L):
-    """Few rows over a long context are split and need a workspace; without it, or
-    with less of it, the call is refused.  A short context needs none."""
+    """Few rows are shared out among workers and need a workspace; without it, or
+    with less of it, the call is refused.  Many rows over a short context need none."""
     a = attention(tokens=1, sequences=1, max_tokens=1, max_context=100000, mask_words=0)
     need = L.quik_attention_workspace_size(ctypes.byref(a), ctypes.byref(cache()))
     assert need > 0
     for ws, n in ((None, 1 << 40), (G, need - 1), (ODD, 1 << 40)):
         assert attend(L, a, cache(), mask=None, ws=ws, n=n) == q.QUIK_ERR_INVALID_ARG
-    a = attention(tokens=1, sequences=1, max_tokens=1, max_context=20, mask_words=0)
+    a = attention(tokens=64, sequences=1, max_tokens=64, max_context=20, mask_words=2)
     assert L.quik_attention_workspace_size(ctypes.byref(a), ctypes.byref(cache())) == 0
 
 

@@ -399,21 +399,26 @@ def test_indices_out_of_range_are_reported():
     """Bad pages, lengths, slots and positions are never used as addresses: the
     call completes, the rest of its results stand, and the check reports it."""
     c = Case(8, 64, 2, 1, 16, [40, 20], [2, 2], False, seed=19)
-    good, _ = c.check()
+    c.check()
+    o, _, bo, _ = c.reference()
+    # the other sequence's rows: right whatever this one holds (their last bits
+    # go by how all the tokens of the call are shared out)
+    stands = lambda out: within(out[:2], o[:2], bo[:2])  # noqa: E731
     want = c.table.copy()
     for bad in (-1, c.cache.pages, 1 << 30):
         c.table = want.copy()
         c.table[1, 0] = bad
         out, _ = c.run()
         assert q.quik_sync_check() == q.QUIK_ERR_INVALID_ARG
-        assert torch.equal(out[:2], good[:2]) and torch.isfinite(out).all()
+        stands(out)
+        assert torch.isfinite(out).all()
     c.table = want
     for field, value in (("ctx", -5), ("ctx", 1 << 30)):
         keep = c.ctx.copy()
         c.ctx[1] = value
         out, _ = c.run(max_context=64)
         assert q.quik_sync_check() == q.QUIK_ERR_INVALID_ARG
-        assert torch.equal(out[:2], good[:2])
+        stands(out)
         c.ctx = keep
     for cu in ([0, 2, 1], [-3, 2, 4], [0, 2, 900], [0, 4, 4]):
         keep = c.cu.copy()
