@@ -749,18 +749,6 @@ __device__ __forceinline__ Load load_of(const Params &p, const Seq &s) {
     return l;
 }
 
-// Sum of the tiles of sequences [0, n) (whole warp; every lane gets it).
-__device__ __forceinline__ int64_t tiles_before(const Params &p, int n, bool report) {
-    int64_t sum = 0;
-    for (int b = threadIdx.x % 32; b < n; b += 32) {
-        const Load l = load_of(p, sequence(p, b, report));
-        sum += static_cast<int64_t>(l.tiles) * l.items;
-    }
-#pragma unroll
-    for (int x = 1; x < 32; x *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    return sum;
-}
-
 // A place in the work: an item of sequence b and a tile of it.
 struct Cursor {
     int b, item, tile, tiles, items;
@@ -783,8 +771,20 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int worker = blockIdx.x * C::NW + warp;
 
-    // ---- this worker's run
-    const int64_t all = tiles_before(p, p.sequences, blockIdx.x == 0 && warp == 0);
+    // ---- this worker's run: the tiles of all sequences, 32 sequences at a time
+    // (the first 32 are looked at once: the usual number, and this is latency)
+    const bool report = blockIdx.x == 0 && warp == 0;
+    Seq mine{};
+    if (lane < p.sequences) mine = sequence(p, lane, report);
+    const Load mine_load = load_of(p, mine);
+    const int64_t mine_tiles = static_cast<int64_t>(mine_load.tiles) * mine_load.items;
+    int64_t all = mine_tiles;
+    for (int b = 32 + lane; b < p.sequences; b += 32) {
+        const Load l = load_of(p, sequence(p, b, report));
+        all += static_cast<int64_t>(l.tiles) * l.items;
+    }
+#pragma unroll
+    for (int x = 1; x < 32; x *= 2) all += __shfl_xor_sync(0xffffffffu, all, x);
     // no more workers than tiles: every worker between an item's first and last has a piece of it
     const int64_t workers = all < p.workers ? all : p.workers;
     if (worker >= workers) return;
@@ -795,12 +795,12 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel
     {
         int64_t before = 0;
         for (int b0 = 0; b0 < p.sequences; b0 += 32) {
-            int64_t mine = 0;
-            if (b0 + lane < p.sequences) {
-                const Load l = load_of(p, sequence(p, b0 + lane, false));
-                mine = static_cast<int64_t>(l.tiles) * l.items;
+            int64_t own = mine_tiles;
+            if (b0 > 0) {
+                const Load l = load_of(p, b0 + lane < p.sequences ? sequence(p, b0 + lane, false) : Seq{});
+                own = static_cast<int64_t>(l.tiles) * l.items;
             }
-            int64_t to = mine;  // tiles up to and with this lane's sequence
+            int64_t to = own;  // tiles up to and with this lane's sequence
 #pragma unroll
             for (int x = 1; x < 32; x *= 2) {
                 const int64_t y = __shfl_up_sync(0xffffffffu, to, x);
@@ -810,16 +810,27 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel
             const unsigned past = __ballot_sync(0xffffffffu, to > from);
             if (past != 0) {
                 const int src = __ffs(past) - 1;
-                const int64_t begin = __shfl_sync(0xffffffffu, to - mine, src);
-                enter(p, at, b0 + src);
-                at.item = static_cast<int>((from - begin) / at.tiles);
-                at.tile = static_cast<int>((from - begin) % at.tiles);
+                const int64_t ahead = from - __shfl_sync(0xffffffffu, to - own, src);
+                if (b0 == 0) {
+                    at.b = src;
+                    at.sq.first = __shfl_sync(0xffffffffu, mine.first, src);
+                    at.sq.n = __shfl_sync(0xffffffffu, mine.n, src);
+                    at.sq.ctx = __shfl_sync(0xffffffffu, mine.ctx, src);
+                    at.sq.total = __shfl_sync(0xffffffffu, mine.total, src);
+                    const Load l = load_of(p, at.sq);
+                    at.tiles = l.tiles, at.items = l.items;
+                } else {
+                    enter(p, at, b0 + src);
+                }
+                at.item = static_cast<int>(ahead / at.tiles);
+                at.tile = static_cast<int>(ahead % at.tiles);
                 break;
             }
             before = __shfl_sync(0xffffffffu, to, 31);
         }
     }
     int todo = left;
+    const int first_b = at.b, first_item = at.item;
 
     uint8_t *ring = smem + warp * C::STAGES * C::STAGE;
     // of the place to be issued next: its rows, its page number
@@ -870,6 +881,61 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel
     float o[C::MT][4], m[2], l[2];
     int R = 0;
 
+    // A new item: this lane's query row is q8, and of it the channels that the
+    // lanes' K words give up together.
+    auto open = [&](int b, int item) {
+        first = p.cu[b];
+        const int rows = (p.cu[b + 1] - first) * p.group, blocks = (rows + 7) / 8;
+        const int h = item / blocks, r0 = item % blocks * 8;
+        const int r = r0 + q8;
+        const bool ok = r < rows;
+        const uint16_t *row = p.q;
+        if (ok)
+            row += static_cast<int64_t>(first + r / p.group) * p.q_stride +
+                   static_cast<int64_t>(h * p.group + r % p.group) * D;
+        if constexpr (BITS == 16) {
+#pragma unroll
+            for (int s = 0; s < C::STEPS; ++s)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    qf[s][x] = ok ? *reinterpret_cast<const uint32_t *>(row + 16 * s + 8 * x + 2 * q4) : 0u;
+        } else {
+            uint32_t w[D / 8];
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (ok) u = *reinterpret_cast<const uint4 *>(row + q4 * (D / 4) + 8 * i);
+                w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+            }
+#pragma unroll
+            for (int s = 0; s < C::STEPS; ++s) {
+                if constexpr (BITS == 8) {
+                    qf[s][0] = w[2 * s], qf[s][1] = w[2 * s + 1];
+                } else {
+                    // words of eight channels: step 2 i even nibbles (0, 4), (2, 6), step 2 i + 1
+                    // odd ones (1, 5), (3, 7)
+                    const int i = 4 * (s / 2);
+                    const uint32_t sel = s % 2 ? 0x7632u : 0x5410u;
+                    qf[s][0] = pick(w[i], w[i + 2], sel), qf[s][1] = pick(w[i + 1], w[i + 3], sel);
+                }
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int x = r0 + 2 * q4 + e;
+            tok[e] = x < rows ? x / p.group : -1;
+            m[e] = -INFINITY, l[e] = 0.0f;
+        }
+        R = -100;
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
+    };
+    // (of the first item while its first tile is on the way)
+    open(first_b, first_item);
+    bool opened = true;
+
     int stage = 0;
     for (; todo > 0; --todo) {
         copy_wait<C::STAGES - 2>();
@@ -883,57 +949,8 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel
         const unsigned live = *reinterpret_cast<const unsigned *>(tail + C::SCALES);
         const int4 place = *reinterpret_cast<const int4 *>(tail + C::SCALES + 16);
         const int j0 = place.x;
-        if (place.w & 1) {
-            // ---- a new item: this lane's query row is q8, and of it the channels
-            // that the lanes' K words give up together
-            first = p.cu[place.z];
-            const int rows = (p.cu[place.z + 1] - first) * p.group, blocks = (rows + 7) / 8;
-            const int h = place.y / blocks, r0 = place.y % blocks * 8;
-            const int r = r0 + q8;
-            const bool ok = r < rows;
-            const uint16_t *row = p.q;
-            if (ok)
-                row += static_cast<int64_t>(first + r / p.group) * p.q_stride +
-                       static_cast<int64_t>(h * p.group + r % p.group) * D;
-            if constexpr (BITS == 16) {
-#pragma unroll
-                for (int s = 0; s < C::STEPS; ++s)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-                        qf[s][x] = ok ? *reinterpret_cast<const uint32_t *>(row + 16 * s + 8 * x + 2 * q4) : 0u;
-            } else {
-                uint32_t w[D / 8];
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    uint4 u = make_uint4(0, 0, 0, 0);
-                    if (ok) u = *reinterpret_cast<const uint4 *>(row + q4 * (D / 4) + 8 * i);
-                    w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
-                }
-#pragma unroll
-                for (int s = 0; s < C::STEPS; ++s) {
-                    if constexpr (BITS == 8) {
-                        qf[s][0] = w[2 * s], qf[s][1] = w[2 * s + 1];
-                    } else {
-                        // words of eight channels: step 2 i even nibbles (0, 4), (2, 6), step 2 i + 1
-                        // odd ones (1, 5), (3, 7)
-                        const int i = 4 * (s / 2);
-                        const uint32_t sel = s % 2 ? 0x7632u : 0x5410u;
-                        qf[s][0] = pick(w[i], w[i + 2], sel), qf[s][1] = pick(w[i + 1], w[i + 3], sel);
-                    }
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int x = r0 + 2 * q4 + e;
-                tok[e] = x < rows ? x / p.group : -1;
-                m[e] = -INFINITY, l[e] = 0.0f;
-            }
-            R = -100;
-#pragma unroll
-            for (int i = 0; i < C::MT; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
-        }
+        if ((place.w & 1) && !opened) open(place.z, place.y);
+        opened = false;
 
         // ---- S^T: s[i][2 f + e] is token 16 i + 8 f + q8, row 2 q4 + e
         float s[2][4];
@@ -1183,15 +1200,18 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel
     }
 }
 
-// Join an item's pieces: a block of 4 D threads a row, thread (k, d) every
-// fourth piece's channel d.
+// Join an item's pieces: a block of four warps a row, each warp every fourth
+// piece.  A lane's 16 bytes of a piece hold two channels of this row (and of
+// the row beside it); up to 16 pieces are loaded at once, before their maximum
+// is known.
 template <class C>
-__global__ void __launch_bounds__(4 * C::D) tree_attention_few_join_kernel(const Params p) {
-    constexpr int D = C::D;
-    __shared__ float acc_s[4][D], sum_s[4], max_s[4 * D / 32];
+__global__ void __launch_bounds__(128) tree_attention_few_join_kernel(const Params p) {
+    constexpr int D = C::D, V = D / 64, AHEAD = 4;
+    __shared__ float acc_s[4][D], sum_s[4], max_s[4];
     const int h = blockIdx.y, b = blockIdx.z, g = blockIdx.x;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const Seq sq = sequence(p, b, false);  // (not written by the kernel that is waited for)
     ptx::grid_dependency_wait();
-    const Seq sq = sequence(p, b, false);
     if (g >= sq.n * p.group) return;
     const Load ld = load_of(p, sq);
     const int r = g % 8, item = h * (ld.items / p.heads) + g / 8;
@@ -1199,35 +1219,62 @@ __global__ void __launch_bounds__(4 * C::D) tree_attention_few_join_kernel(const
     const int64_t index = b * (p.heads * blocks) + item;
     int w0 = 0, count = 0;
     if (ld.tiles > 0) {
-        w0 = p.item_span[2 * index];
-        count = p.item_span[2 * index + 1] - w0 + 1;
+        const int2 span = *reinterpret_cast<const int2 *>(p.item_span + 2 * index);
+        w0 = span.x;
+        count = span.y - span.x + 1;
     }
     const int64_t piece0 = index + w0;
+    const float2 *ml = p.piece_ml + piece0 * 8 + r;
+    // tile c of the products, channel q8: lanes (c, q8), 4 tiles a load
+    const int q8 = lane % 8, c0 = lane / 8;
+    const float4 *src = p.piece_o + (piece0 * C::MT + c0) * 32 + q8 * 4 + r / 2;
+    float2 a[AHEAD];
+    float4 v[AHEAD][V];
     float M = -INFINITY;
-    for (int s = threadIdx.x; s < count; s += 4 * D) M = fmaxf(M, p.piece_ml[(piece0 + s) * 8 + r].x);
 #pragma unroll
-    for (int x = 1; x < 32; x *= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-    if (threadIdx.x % 32 == 0) max_s[threadIdx.x / 32] = M;
-    __syncthreads();
+    for (int i = 0; i < AHEAD; ++i) {
+        const int s = warp + 4 * i;
+        const bool ok = s < count;
+        a[i] = ok ? ml[s * 8] : make_float2(-INFINITY, 0.0f);
 #pragma unroll
-    for (int x = 0; x < 4 * D / 32; ++x) M = fmaxf(M, max_s[x]);
-    const float base = M == -INFINITY ? 0.0f : M;
-    // where the lanes hold channel d of row r
-    const int k = threadIdx.x / D, d = threadIdx.x % D;
-    const int q8 = C::BITS == 16 ? d % 8 : d / (D / 8);
-    const int c = C::BITS == 16 ? d / 16 : d % (D / 8) / 2, x = C::BITS == 16 ? d / 8 % 2 : d % 2;
-    const float *src = reinterpret_cast<const float *>(p.piece_o) +
-                       ((piece0 * C::MT + c) * 32 + q8 * 4 + r / 2) * 4 + 2 * x + r % 2;
-    float acc = 0.0f, L = 0.0f;
-#pragma unroll 8
-    for (int s = k; s < count; s += 4) {
-        const float2 a = p.piece_ml[(piece0 + s) * 8 + r];
-        const float f = exp2_fast(a.x - base);
-        acc = fmaf(f, src[static_cast<int64_t>(s) * (C::MT * 128)], acc);
-        L = fmaf(f, a.y, L);
+        for (int j = 0; j < V; ++j)
+            v[i][j] = ok ? src[static_cast<int64_t>(s) * (C::MT * 32) + j * 128] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        M = fmaxf(M, a[i].x);
     }
-    acc_s[k][d] = acc;
-    if (d == 0) sum_s[k] = L;
+    for (int s = 4 * AHEAD + threadIdx.x; s < count; s += 128) M = fmaxf(M, ml[s * 8].x);
+#pragma unroll
+    for (int y = 1; y < 32; y *= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, y));
+    if (lane == 0) max_s[warp] = M;
+    __syncthreads();
+    M = fmaxf(fmaxf(max_s[0], max_s[1]), fmaxf(max_s[2], max_s[3]));
+    const float base = M == -INFINITY ? 0.0f : M;
+    float acc[V][2] = {}, L = 0.0f;
+    auto add = [&](const float2 &m, const float4 (&x)[V]) {
+        const float f = exp2_fast(m.x - base);
+        L = fmaf(f, m.y, L);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            acc[j][0] = fmaf(f, r % 2 ? x[j].y : x[j].x, acc[j][0]);
+            acc[j][1] = fmaf(f, r % 2 ? x[j].w : x[j].z, acc[j][1]);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) add(a[i], v[i]);
+#pragma unroll 4
+    for (int s = 4 * AHEAD + warp; s < count; s += 4) {
+        float4 x[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] = src[static_cast<int64_t>(s) * (C::MT * 32) + j * 128];
+        add(ml[s * 8], x);
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int c = c0 + 4 * j;
+            acc_s[warp][C::BITS == 16 ? 16 * c + 8 * x + q8 : q8 * (D / 8) + 2 * c + x] = acc[j][x];
+        }
+    if (lane == 0) sum_s[warp] = L;
     __syncthreads();
     L = (sum_s[0] + sum_s[1]) + (sum_s[2] + sum_s[3]);
     const int head = h * p.group + g % p.group, token = sq.first + g / p.group;
@@ -1254,8 +1301,8 @@ __global__ void __launch_bounds__(128) tree_attention_join_kernel(const Params p
     __shared__ float acc_s[4][D];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int h = blockIdx.y, b = blockIdx.z;
+    const Seq sq = sequence(p, b, false);  // (not written by the kernel that is waited for)
     ptx::grid_dependency_wait();
-    const Seq sq = sequence(p, b, false);
     const int g = blockIdx.x;
     if (g >= sq.n * p.group) return;
     const int head = h * p.group + g % p.group, token = sq.first + g / p.group;
@@ -1312,7 +1359,8 @@ int few_ctas(int head_dim) {
 }
 
 // Up to eight rows: the transposed form (wr 0), with as many workers as are
-// resident at once, but four tiles or more each where the hint is right.
+// resident at once, or one for each tile (a tile takes a lone warp more than a
+// microsecond: one token over 200, 32 heads: 11.8 us with four tiles a worker).
 // More rows: the fewest row warps that hold them (a warp's products have 16),
 // up to four, and splits of the cached tokens, enough CTAs for about two a
 // resident slot, while each warp group keeps at least four tiles.
@@ -1328,7 +1376,7 @@ Plan plan_of(const AttentionArgs &a) {
         const int ctas = a.cache.kv_type == QUIK_KV_INT4   ? few_ctas<4>(a.cache.head_dim)
                          : a.cache.kv_type == QUIK_KV_INT8 ? few_ctas<8>(a.cache.head_dim)
                                                            : few_ctas<16>(a.cache.head_dim);
-        const int64_t want = (items * tiles + 15) / 16, most = static_cast<int64_t>(sm_count()) * ctas;
+        const int64_t want = (items * tiles + 3) / 4, most = static_cast<int64_t>(sm_count()) * ctas;
         r.workers = 4 * static_cast<int>(want < 1 ? 1 : want < most ? want : most);
         r.pieces = items + r.workers;
         return r;
@@ -1371,7 +1419,7 @@ quik_status run_few(const Params &p, cudaStream_t stream) {
     if (!attribute_set_once(reinterpret_cast<const void *>(kernel), C::SMEM)) return QUIK_ERR_CUDA;
     kernel<<<p.workers / C::NW, C::NW * 32, C::SMEM, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return QUIK_ERR_CUDA;
-    return launch_join(p, &tree_attention_few_join_kernel<C>, 4 * C::D, stream);
+    return launch_join(p, &tree_attention_few_join_kernel<C>, 128, stream);
 }
 
 template <class C>
