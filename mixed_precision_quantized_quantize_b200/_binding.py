@@ -304,46 +304,17 @@ def quik_workspace_size_24(shape: quik_shape) -> int:
     return int(lib().quik_workspace_size_24(ctypes.byref(shape)))
 
 
-# The attention operators' calls take a few microseconds on the GPU, so what the
-# host does for each counts: a tensor's type and device are looked at once (a
-# device index of -1 is the CPU), the stream is read as a raw handle, and the C
-# function is called with plain integers.
-_F16, _F32, _I32, _L64 = torch.float16, torch.float32, torch.int32, torch.int64
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-
-
-def _refuse(t, what, dtype, dev):
-    """Say what is wrong with a tensor that is not of `dtype` on device `dev`."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{what} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{what} must live on a CUDA device")
-    if t.dtype is not dtype:
-        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    raise ValueError(f"{what} is on cuda:{t.get_device()}, others on cuda:{dev}")
-
-
-def _index(t, what):
-    """Index of the CUDA device that a tensor lives on."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{what} must be a torch.Tensor")
-    i = t.get_device()
-    if i < 0:
-        raise ValueError(f"{what} must live on a CUDA device")
-    return i
-
-
-def _rows(t, what, dev=None):
+def _rows(t, what):
     """(pointer, row stride in elements) of fp16 rows [tokens, heads, head_dim]: the heads of a
     token are contiguous, the tokens may be any distance apart (a slice of a projection's output)."""
     if t is None:
         return None, 0
-    if dev is None:
-        dev = _index(t, what)
-    if t.dtype is not _F16 or t.get_device() != dev:
-        _refuse(t, what, _F16, dev)
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must live on a CUDA device")
+    if t.dtype != torch.float16:
+        raise TypeError(f"{what} must be torch.float16, got {t.dtype}")
     if t.dim() != 3:
         raise ValueError(f"{what} must be [tokens, heads, head_dim], got {tuple(t.shape)}")
     n, h, d = t.shape
@@ -353,51 +324,6 @@ def _rows(t, what, dev=None):
     if n == 1:
         sn = -(-h * d // 8) * 8  # the stride of a single row says nothing
     return t.data_ptr() or None, sn
-
-
-def _flat(t, what, dtype, dev):
-    """Pointer of a contiguous tensor of `dtype` on device `dev`."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.get_device() != dev:
-        _refuse(t, what, dtype, dev)
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
-    return t.data_ptr() or None
-
-
-class _on:
-    """Device `index` and `stream` (None: its current one) as the current ones: what is allocated
-    inside belongs to that stream."""
-
-    def __init__(self, index, stream):
-        if stream is not None and stream.device.index != index:
-            raise ValueError(f"stream of {stream.device}, tensors on cuda:{index}")
-        self.contexts = [torch.cuda.device(index)]
-        if stream is not None:
-            self.contexts.append(torch.cuda.stream(stream))
-
-    def __enter__(self):
-        for c in self.contexts:
-            c.__enter__()
-
-    def __exit__(self, *exc):
-        for c in reversed(self.contexts):
-            c.__exit__(*exc)
-
-
-def _tables(cos, sin, positions, tokens):
-    """(rotary_dim, table rows) of the rotation's tables, or (0, 0) without them."""
-    if cos is None and sin is None:
-        return 0, 0
-    if cos is None or sin is None or positions is None:
-        raise ValueError("a rotation needs cos, sin and positions")
-    shape = cos.shape
-    if len(shape) != 2 or shape != sin.shape:
-        raise ValueError("cos and sin must be [rows, rotary_dim / 2], both alike")
-    if positions.shape != (tokens,):
-        raise ValueError(f"positions must be [{tokens}], got {tuple(positions.shape)}")
-    return 2 * shape[1], shape[0]
 
 
 def quik_qk_norm_rope(heads, q, k, q_gamma, k_gamma, eps, cos, sin, positions, q_out, k_out,
@@ -671,6 +597,36 @@ class QuikLinear:
 
 
 # ------------------------------------------------------------------ attention
+_calls = None
+
+
+def _ext():
+    """The extension module that makes the attention calls (loaded once, bound to the library)."""
+    global _calls
+    if _calls is None:
+        L = lib()
+        try:
+            from . import _calls as ext
+        except ImportError as e:
+            raise RuntimeError("the extension module _calls is missing: build it with "
+                               "`python -m mixed_precision_quantized_quantize_b200.build`") from e
+        if ext.torch_version != torch.__version__:
+            raise RuntimeError(f"_calls was built for torch {ext.torch_version}, this is {torch.__version__}: "
+                               "build it again with `--force`")
+        ext.bind(QuikError, *(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
+            "quik_qk_norm_rope", "quik_kv_append", "quik_kv_gather", "quik_attention_workspace_size",
+            "quik_tree_attention")))
+        _calls = ext
+    return _calls
+
+
+def _on(stream, t):
+    """`stream` as the current one of the tensors' device (launches and new tensors go by it)."""
+    if t.is_cuda and stream.device != t.device:
+        raise ValueError(f"stream of {stream.device}, tensors on {t.device}")
+    return torch.cuda.stream(stream)
+
+
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, q_weight=None, k_weight=None,
                  eps: float = 1e-6, cos=None, sin=None, positions=None, interleaved: bool = False,
                  q_out=None, k_out=None, stream=None):
@@ -678,38 +634,11 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, q_weight=None, k_weigh
     rotation by cos / sin fp32 [rows, rotary_dim / 2] at positions int32 [tokens] (None: none), in
     one pass.  q [tokens, q_heads, head_dim] and k fp16, slices of a projection's rows as they are;
     returns (q_out, k_out), new tensors unless given (each may be its input)."""
-    n, qh, d = q.shape
-    kh = 0
-    if k is not None:
-        kn, kh, kd = k.shape
-        if kn != n or kd != d:
-            raise ValueError(f"k must be [{n}, heads, {d}], got {tuple(k.shape)}")
-    rotary, rows = _tables(cos, sin, positions, n)
-    if (q_weight is not None and q_weight.shape != (d,)) or (k_weight is not None and k_weight.shape != (d,)):
-        raise ValueError(f"q_weight and k_weight must be [{d}]")
-    if (q_out is not None and q_out.shape != q.shape) or (k_out is not None and
-                                                          (k is None or k_out.shape != k.shape)):
-        raise ValueError("an output must have its input's shape")
-    dev = _index(q, "q")
-    if stream is not None or dev != _current_device():
-        with _on(dev, stream):
+    if stream is not None:
+        with _on(stream, q):
             return qk_norm_rope(q, k, q_weight, k_weight, eps, cos, sin, positions, interleaved, q_out, k_out)
-    if q_out is None:
-        q_out = q.new_empty((n, qh, d))
-    if k_out is None and k is not None:
-        k_out = k.new_empty((n, kh, d))
-    qp, qs = _rows(q, "q", dev)
-    kp, ks = _rows(k, "k", dev)
-    qo, qos = _rows(q_out, "q_out", dev)
-    ko, kos = _rows(k_out, "k_out", dev)
-    status = (_lib or lib()).quik_qk_norm_rope(
-        quik_heads(n, qh, kh, d, rotary, bool(interleaved), rows), qp, qs, kp, ks,
-        _flat(q_weight, "q_weight", _F16, dev), _flat(k_weight, "k_weight", _F16, dev), eps,
-        _flat(cos, "cos", _F32, dev), _flat(sin, "sin", _F32, dev), _flat(positions, "positions", _I32, dev),
-        qo, qos, ko, kos, _raw_stream(dev))
-    if status:
-        raise QuikError(status, "quik_qk_norm_rope")
-    return q_out, k_out
+    return (_calls or _ext()).qk_norm_rope(q, k, q_weight, k_weight, eps, cos, sin, positions, interleaved, q_out,
+                                           k_out)
 
 
 class QuikKVCache:
@@ -729,16 +658,20 @@ class QuikKVCache:
         pages, heads, page_size, row = k.shape
         if (kind == QUIK_KV_FP16) != (k_scale is None) or (k_scale is None) != (v_scale is None):
             raise ValueError("the quantised types, and only they, have k_scale and v_scale")
-        for s in (k_scale, v_scale):
-            if s is not None and s.shape != (pages, heads, page_size):
-                raise ValueError(f"scales must be [{pages}, {heads}, {page_size}], got {tuple(s.shape)}")
+        for t in (k_scale, v_scale):
+            if t is not None and t.shape != (pages, heads, page_size):
+                raise ValueError(f"scales must be [{pages}, {heads}, {page_size}], got {tuple(t.shape)}")
+        for t in (v, k_scale, v_scale):
+            if t is not None and t.device != k.device:
+                raise ValueError(f"buffers on {k.device} and on {t.device}")
+        # the buffers live as long as this object does: the struct holds their addresses
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.heads, self.head_dim, self.page_size, self.pages = heads, row * per, page_size, pages
-        self.device, self.index = k.device, _index(k, "k")
-        self.struct = quik_kv_cache(kind, heads, row * per, page_size, pages, 0,
-                                    _flat(k, "k", k.dtype, self.index), _flat(v, "v", k.dtype, self.index),
-                                    _flat(k_scale, "k_scale", _F32, self.index),
-                                    _flat(v_scale, "v_scale", _F32, self.index))
+        self.device, self.index = k.device, k.get_device()
+        self.struct = quik_kv_cache(kind, heads, row * per, page_size, pages, 0, _ptr(k, k.dtype, "k"),
+                                    _ptr(v, k.dtype, "v"), _ptr(k_scale, torch.float32, "k_scale"),
+                                    _ptr(v_scale, torch.float32, "v_scale"))
+        self.address = ctypes.addressof(self.struct)
 
     @classmethod
     def empty(cls, pages: int, heads: int, head_dim: int, page_size: int = 64, bits: int = 16,
@@ -759,49 +692,18 @@ class QuikKVCache:
                positions=None, interleaved: bool = False, stream=None) -> None:
         """quik_kv_append: rows k, v fp16 [tokens, heads, head_dim] into slots int64 [tokens]
         (negative: left out), the keys rotated by cos / sin at positions on the way."""
-        n = k.shape[0]
-        if k.shape != (n, self.heads, self.head_dim) or v.shape != k.shape:
-            raise ValueError(f"k and v must be [tokens, {self.heads}, {self.head_dim}], got "
-                             f"{tuple(k.shape)} and {tuple(v.shape)}")
-        if slots.shape != (n,):
-            raise ValueError(f"slots must be [{n}], got {tuple(slots.shape)}")
-        rotary, rows = _tables(cos, sin, positions, n)
-        dev = self.index
-        if stream is not None or dev != _current_device():
-            with _on(dev, stream):
+        if stream is not None:
+            with _on(stream, self.k):
                 return self.append(k, v, slots, cos, sin, positions, interleaved)
-        kp, ks = _rows(k, "k", dev)
-        vp, vs = _rows(v, "v", dev)
-        status = (_lib or lib()).quik_kv_append(
-            quik_heads(n, 0, self.heads, self.head_dim, rotary, bool(interleaved), rows), self.struct, kp, ks,
-            vp, vs, _flat(cos, "cos", _F32, dev), _flat(sin, "sin", _F32, dev),
-            _flat(positions, "positions", _I32, dev), _flat(slots, "slots", _L64, dev), _raw_stream(dev))
-        if status:
-            raise QuikError(status, "quik_kv_append")
+        return (_calls or _ext()).kv_append(self.address, self.index, k, v, slots, cos, sin, positions, interleaved)
 
     def gather(self, slots: torch.Tensor, k_out=None, v_out=None, stream=None):
-        """quik_kv_gather: (k, v) fp16 [tokens, heads, head_dim] of slots int64 [tokens]."""
-        if slots.dim() != 1:
-            raise ValueError(f"slots must be [tokens], got {tuple(slots.shape)}")
-        shape = (slots.shape[0], self.heads, self.head_dim)
-        for o in (k_out, v_out):
-            if o is not None and o.shape != shape:
-                raise ValueError(f"outputs must be {shape}, got {tuple(o.shape)}")
-        dev = self.index
-        if stream is not None or dev != _current_device():
-            with _on(dev, stream):
+        """quik_kv_gather: (k, v) fp16 [tokens, heads, head_dim] of slots int64 [tokens] (a
+        negative slot: zeros)."""
+        if stream is not None:
+            with _on(stream, self.k):
                 return self.gather(slots, k_out, v_out)
-        if k_out is None:
-            k_out = torch.empty(shape, dtype=_F16, device=self.device)
-        if v_out is None:
-            v_out = torch.empty(shape, dtype=_F16, device=self.device)
-        kp, ks = _rows(k_out, "k_out", dev)
-        vp, vs = _rows(v_out, "v_out", dev)
-        status = (_lib or lib()).quik_kv_gather(self.struct, shape[0], _flat(slots, "slots", _L64, dev), kp, ks, vp,
-                                                vs, _raw_stream(dev))
-        if status:
-            raise QuikError(status, "quik_kv_gather")
-        return k_out, v_out
+        return (_calls or _ext()).kv_gather(self.address, self.index, slots, k_out, v_out)
 
 
 def tree_attention(q: torch.Tensor, cache: QuikKVCache, page_table: torch.Tensor,
@@ -816,41 +718,9 @@ def tree_attention(q: torch.Tensor, cache: QuikKVCache, page_table: torch.Tensor
     head_dim ** -0.5.  Returns out [tokens, q_heads, head_dim], with return_lse (out, lse fp32
     [tokens, q_heads]).  Rows that belong to no sequence are left as they were (in new tensors:
     undefined)."""
-    n, qh, d = q.shape
-    if d != cache.head_dim:
-        raise ValueError(f"q must have heads of {cache.head_dim}, got {d}")
-    B, width = page_table.shape
-    if context.shape != (B,) or cu_tokens.shape != (B + 1,):
-        raise ValueError("context must be [sequences], page_table [sequences, max_pages], cu_tokens "
-                         "[sequences + 1]")
-    words = 0
-    if mask is not None:
-        rows, words = mask.shape
-        if rows != n:
-            raise ValueError(f"mask must be [{n}, words], got {tuple(mask.shape)}")
-    if out is not None and out.shape != q.shape:
-        raise ValueError("out must have the shape of q")
-    if lse is not None and lse.shape != (n, qh):
-        raise ValueError(f"lse must be [{n}, {qh}], got {tuple(lse.shape)}")
-    dev = cache.index
-    if stream is not None or dev != _current_device():
-        with _on(dev, stream):
+    if stream is not None:
+        with _on(stream, q):
             return tree_attention(q, cache, page_table, context, cu_tokens, max_tokens, max_context, mask, scale,
                                   out, lse, return_lse)
-    qp, qs = _rows(q, "q", dev)
-    if out is None:
-        out = q.new_empty((n, qh, d))
-    if lse is None and return_lse:
-        lse = torch.empty((n, qh), dtype=_F32, device=cache.device)
-    op, os_ = _rows(out, "out", dev)
-    a = quik_attention(n, B, qh, max_tokens, width, max_context, words, d ** -0.5 if scale is None else scale)
-    L = _lib or lib()
-    need = L.quik_attention_workspace_size(a, cache.struct)
-    ws = torch.empty(need, dtype=torch.uint8, device=cache.device) if need else None
-    status = L.quik_tree_attention(
-        a, cache.struct, qp, qs, _flat(page_table, "page_table", _I32, dev), _flat(context, "context", _I32, dev),
-        _flat(cu_tokens, "cu_tokens", _I32, dev), _flat(mask, "mask", _I32, dev), op, os_,
-        _flat(lse, "lse", _F32, dev), ws.data_ptr() if need else None, need, _raw_stream(dev))
-    if status:
-        raise QuikError(status, "quik_tree_attention")
-    return (out, lse) if return_lse else out
+    return (_calls or _ext()).tree_attention(q, cache.address, cache.index, page_table, context, cu_tokens,
+                                             max_tokens, max_context, mask, scale, out, lse, return_lse)

@@ -20,6 +20,9 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libquik_b200.so")
 # self-checking variant (-DQUIK_CHECKS): bounds checks that record and skip
 LIB_CHECKED = os.path.join(HERE, "libquik_b200_checked.so")
+# the attention calls from Python (a CPython extension over torch's C++ API)
+CALLS_SRC = os.path.join(CSRC, "torch_calls.cpp")
+CALLS = os.path.join(HERE, "_calls.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -52,8 +55,32 @@ def nvcc() -> str:
     return "nvcc"
 
 
+def build_calls(force: bool = False) -> str:
+    """The extension module _calls: host code only, for the torch that is installed."""
+    deps = [CALLS_SRC, os.path.join(ROOT, "include", "quik.h"), __file__]
+    if not force and os.path.exists(CALLS) and all(os.path.getmtime(d) <= os.path.getmtime(CALLS) for d in deps):
+        return CALLS
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc())) if os.path.isabs(nvcc()) else "/usr/local/cuda"
+    tmp = CALLS + f".tmp{os.getpid()}"
+    subprocess.check_call([
+        os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+        f'-DQUIK_TORCH_VERSION="{torch.__version__}"',
+        "-I", os.path.join(base, "include"), "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+        "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
+        # the C++ runtime before torch's libraries, which carry parts of one of their own
+        CALLS_SRC, "-o", tmp, "-Wl,--no-as-needed", "-l:libstdc++.so.6", "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(force: bool = False, verbose: bool = False, checks: bool = False) -> str:
     lib = LIB_CHECKED if checks else LIB
+    build_calls(force and not checks)
     if not force and up_to_date(lib):
         return lib
     tmp = lib + f".tmp{os.getpid()}"
