@@ -452,8 +452,11 @@ quik_status quik_gemm_i32_debug(const quik_shape *shape, const void *Xq, const v
 quik_status quik_sync_check(quik_stream_t stream) {
     // both sets of counters are read, so that neither keeps an old report
     const quik_status st = quik::sync_check(static_cast<cudaStream_t>(stream));
-    const unsigned int rows = quik::take_row_errors(), pages = quik::take_attention_errors();
-    return st == QUIK_OK && (rows != 0 || pages != 0) ? QUIK_ERR_INVALID_ARG : st;
+    unsigned int waits = 0;
+    const unsigned int bad =
+        quik::take_row_errors() + quik::take_attention_errors() + quik::take_wide_errors(&waits);
+    if (st == QUIK_ERR_CUDA || st == QUIK_ERR_TIMEOUT) return st;
+    return waits != 0 ? QUIK_ERR_TIMEOUT : bad != 0 ? QUIK_ERR_INVALID_ARG : st;
 }
 
 quik_status quik_selftest_timeout(uint32_t limit_us, quik_stream_t stream) {

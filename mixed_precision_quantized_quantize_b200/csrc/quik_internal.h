@@ -78,7 +78,8 @@ cudaError_t launch_expand24(const uint8_t *Qs, const uint8_t *meta, int rows, in
 // its start learns of every error recorded since.  A check reports the
 // increase since the previous check of the same counter on the current device.
 enum { kCounterGemmWaits = 0, kCounterQuantWaits = 1, kCounterBadPerm = 2, kCounterPGemmWaits = 3,
-       kCounterBadRow = 4, kCounterBadPage = 5, kCounters = 6 };
+       kCounterBadRow = 4, kCounterBadPage = 5, kCounterWideWaits = 6, kCounterWidePage = 7,
+       kCounters = 8 };
 unsigned counter_increase(int counter, unsigned value);
 // Expired waits in the quantise kernels since the last check (returned), and
 // perm entries outside [0, K) met since the last check (in *bad_perm when
@@ -197,6 +198,8 @@ quik_status launch_tree_attention(const AttentionArgs &a, cudaStream_t stream);
 // Page numbers, lengths and offsets out of range met by the attention kernel
 // since the last check.
 unsigned int take_attention_errors();
+// The same of its tcgen05 form, and its expired waits (in *waits).
+unsigned int take_wide_errors(unsigned int *waits);
 
 quik_status sync_check(cudaStream_t stream);
 quik_status launch_timeout_selftest(uint32_t limit_us, cudaStream_t stream);

@@ -15,135 +15,17 @@
 // their scale multiplies p in fp32 before that rounding, relative to a running
 // power of two 2^R above every scale met so far (O then is in units of 2^R), so
 // p stays within fp16 whatever the scales are.
-#include "quik_internal.h"
-#include "sm100.cuh"
-
-#include <cuda_fp16.h>
+#include "attention.cuh"
 
 namespace quik {
 
-// Indices out of range met by the kernel (page numbers, lengths, offsets):
-// only ever grows; quik_sync_check reports the increase.
-__device__ unsigned int g_attn_bad_index;
-
 namespace {
 
+using Params = AttnParams;
 constexpr int kTile = 32;          // cached tokens per tile
 constexpr float kShift = 14.0f;    // p carries 2^14
 constexpr int kMaxSplits = 64;
-
-struct Params {
-    int tokens, sequences, q_heads, heads, group, max_tokens, max_pages, mask_words;
-    int pages, page_shift, splits, row_blocks;
-    float scale_log2;
-    const uint16_t *q;
-    int64_t q_stride;
-    const uint8_t *k, *v;
-    const float *ks, *vs;
-    const int32_t *page_table, *context, *cu;
-    const uint32_t *mask;
-    uint16_t *out;
-    int64_t out_stride;
-    float *lse;
-    float *part_o;   // [splits][tokens * q_heads][D]
-    float2 *part_ml; // [splits][tokens * q_heads]
-    // up to 8 rows: pieces (workers + items of them), each 8 rows as the warps hold them
-    int workers;
-    float4 *piece_o;   // [pieces][D / 16][32]
-    float2 *piece_ml;  // [pieces][8]
-    int *item_span;    // [items][2]: the workers that hold an item's first and last tile
-};
-
-__device__ __forceinline__ uint32_t smem_addr(const void *p) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-// 16 (or 4) bytes global -> shared, zeros where !ok (nothing is read then).
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool ok) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool ok) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void group_sync(int id, int threads) {
-    if (threads == 32)
-        __syncwarp();
-    else
-        asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t pick(uint32_t a, uint32_t b, uint32_t sel) {
-    uint32_t r;
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
-    return r;
-}
-__device__ __forceinline__ uint32_t half2_sub(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void load_matrix4(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void load_matrix4_t(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-template <int BYTES>
-__device__ __forceinline__ void load_words(uint32_t (&w)[BYTES / 4], uint32_t addr) {
-    if constexpr (BYTES == 16)
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "r"(addr)
-                     : "memory");
-    else if constexpr (BYTES == 8)
-        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
-    else
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
-}
-
-// Codes to fp16, exactly: a code's bits, its sign bit flipped (that adds 128 or
-// 8), are put into the mantissa of 2^10 (or, four bits up, of 2^6), and that
-// base plus the offset is subtracted.  (Without the subtraction, the codes as
-// fp16 subnormals and the offset taken off the sums, a product lost up to ten
-// bits: the tensor cores align subnormals by their nominal exponent.)
-// bytes 0, 1 (hi: 2, 3) of x, already ^ 0x80808080, as a pair
-__device__ __forceinline__ uint32_t pair8(uint32_t x, bool hi) {
-    return half2_sub(pick(x, 0x64006400u, hi ? 0x5352u : 0x5150u), 0x64806480u);  // 1024 + 128
-}
-// the nibbles at bits 0 and 16 (up: 4 and 20) of x as a pair
-__device__ __forceinline__ uint32_t pair4(uint32_t x, bool up) {
-    const uint32_t c = up ? 0x54805480u : 0x64086408u;  // 64 + 8, 1024 + 8
-    uint32_t r;  // (x & mask) ^ c
-    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(x), "r"(up ? 0x00f000f0u : 0x000f000fu), "r"(c));
-    return half2_sub(r, c);
-}
+constexpr int kWideRows = 64;      // more rows of a key head than this: the tcgen05 form
 
 // WR warps share a tile, 16 rows each; NW / WR such groups take tiles in turn.
 template <int BITS_, int D_, int WR_, int NW_>
@@ -168,30 +50,6 @@ struct Cfg {
     static constexpr int STEPS = D / 16;  // products along a head
     static constexpr int NT = D / 8;      // output column tiles
 };
-
-// What a sequence holds; n == 0: nothing to do.
-struct Seq {
-    int first, n, ctx, total;
-};
-__device__ __forceinline__ Seq sequence(const Params &p, int b, bool report) {
-    Seq s;
-    s.first = p.cu[b];
-    const int end = p.cu[b + 1];
-    s.ctx = p.context[b];
-    const int64_t cap = min(static_cast<int64_t>(p.max_pages) << p.page_shift,
-                            static_cast<int64_t>(0x7fffff00));
-    int64_t total = static_cast<int64_t>(s.ctx) + (static_cast<int64_t>(end) - s.first);
-    bool bad = s.first < 0 || end < s.first || end > p.tokens || s.ctx < 0;
-    if (!bad) bad = end - s.first > p.max_tokens;
-    s.n = bad ? 0 : end - s.first;
-    if (!bad && total > cap) {
-        total = cap;
-        if (report) atomicAdd(&g_attn_bad_index, 1u);
-    }
-    if (bad && report) atomicAdd(&g_attn_bad_index, 1u);
-    s.total = bad ? 0 : static_cast<int>(total);
-    return s;
-}
 
 // The cached rows of one sequence and key head, tile by tile, into a ring of
 // stages in shared memory.  TH threads (a warp, or the WR warps that share a
@@ -289,32 +147,6 @@ __device__ __forceinline__ Tiles<C> tiles_of(const Params &p, const Seq &sq, int
     t.page_shift = p.page_shift, t.pages = p.pages;
     t.end = end, t.total = sq.total, t.gt = gt, t.report = report;
     return t;
-}
-
-// Which of the 32 tokens from new token j0 on (negative: context) new token
-// `tok` sees; tok < 0 (no such row): all of them.
-__device__ __forceinline__ unsigned seen(const Params &p, int first, int tok, int j0) {
-    if (tok < 0 || j0 + kTile <= 0) return 0xffffffffu;
-    if (p.mask == nullptr) {
-        const int top = tok - j0;  // last visible position of the tile
-        return top < 0 ? 0u : top >= 31 ? 0xffffffffu : (2u << top) - 1u;
-    }
-    const uint32_t *row = p.mask + static_cast<int64_t>(first + tok) * p.mask_words;
-    if (j0 < 0) return (row[0] << -j0) | ((1u << -j0) - 1u);
-    const int w = j0 / 32;
-    const uint32_t lo = w < p.mask_words ? row[w] : 0u;
-    const uint32_t hi = w + 1 < p.mask_words ? row[w + 1] : 0u;
-    return __funnelshift_r(lo, hi, j0 % 32);
-}
-
-// The unit of the values' scales: the exponent above the largest finite one
-// (given by its bits).
-__device__ __forceinline__ int top_exponent(unsigned top) {
-    return min(max(static_cast<int>(top >> 23) - 126, -100), 126);
-}
-__device__ __forceinline__ unsigned finite_bits(float x) {
-    const unsigned u = __float_as_uint(x) & 0x7fffffffu;
-    return u < 0x7f800000u ? u : 0u;
 }
 
 // Four channels from d on of row r of a block (row g of its sequence): the
@@ -1348,6 +1180,7 @@ __global__ void __launch_bounds__(128) tree_attention_join_kernel(const Params p
 
 // ------------------------------------------------------------------ host side
 struct Plan {
+    int wide;         // > 0: the tcgen05 form, with so many blocks of 128 rows a CTA
     int wr, row_blocks, splits;
     int workers;      // up to 8 rows: warps that share the tiles
     int64_t pieces;
@@ -1372,6 +1205,20 @@ Plan plan_of(const AttentionArgs &a) {
     r.row_blocks = static_cast<int>((rows + block - 1) / block);
     const int64_t items = static_cast<int64_t>(a.sequences) * a.cache.heads * r.row_blocks;
     const int64_t tiles = (static_cast<int64_t>(a.max_context) + a.max_tokens + kTile - 1) / kTile;
+    if (rows > kWideRows) {
+        r.wide = rows <= 128 ? 1 : 2;
+        r.row_blocks = static_cast<int>((rows + 128 * r.wide - 1) / (128 * r.wide));
+        const int64_t ctas = static_cast<int64_t>(a.sequences) * a.cache.heads * r.row_blocks;
+        // one CTA an SM: the number of splits with the least time, counted in tiles
+        // of 64 tokens (start and end of a CTA about four, joining about six)
+        const int64_t sms = sm_count(), long_tiles = (tiles + 1) / 2;
+        int64_t best = INT64_MAX;
+        for (int s = 1; s <= kMaxSplits && (s == 1 || long_tiles >= 4 * s); ++s) {
+            const int64_t cost = (ctas * s + sms - 1) / sms * ((long_tiles + s - 1) / s + 4) + (s > 1 ? 6 : 0);
+            if (cost < best) best = cost, r.splits = s;
+        }
+        return r;
+    }
     if (r.wr == 0) {
         const int ctas = a.cache.kv_type == QUIK_KV_INT4   ? few_ctas<4>(a.cache.head_dim)
                          : a.cache.kv_type == QUIK_KV_INT8 ? few_ctas<8>(a.cache.head_dim)
@@ -1391,7 +1238,7 @@ Plan plan_of(const AttentionArgs &a) {
 }
 
 size_t partial_bytes(const AttentionArgs &a, const Plan &r) {
-    if (r.wr == 0)
+    if (r.wide == 0 && r.wr == 0)
         return static_cast<size_t>(r.pieces) * 8 * (a.cache.head_dim * 4 + 8) +
                static_cast<size_t>(r.pieces - r.workers) * 8;
     if (r.splits == 1) return 0;
@@ -1488,6 +1335,12 @@ quik_status launch_tree_attention(const AttentionArgs &a, cudaStream_t stream) {
     p.piece_o = reinterpret_cast<float4 *>(a.partial);
     p.piece_ml = reinterpret_cast<float2 *>(a.partial + static_cast<size_t>(plan.pieces) * 8 * a.cache.head_dim);
     p.item_span = reinterpret_cast<int *>(p.piece_ml + plan.pieces * 8);
+    if (plan.wide > 0) {
+        const quik_status st = launch_attention_wide(p, a.cache.kv_type, a.cache.head_dim, plan.wide, stream);
+        if (st != QUIK_OK || p.splits == 1) return st;
+        return launch_join(p, a.cache.head_dim == 64 ? &tree_attention_join_kernel<64> : &tree_attention_join_kernel<128>,
+                           128, stream);
+    }
     if (a.cache.kv_type == QUIK_KV_INT4) return run_dim<4>(p, a.cache.head_dim, plan.wr, stream);
     if (a.cache.kv_type == QUIK_KV_INT8) return run_dim<8>(p, a.cache.head_dim, plan.wr, stream);
     return run_dim<16>(p, a.cache.head_dim, plan.wr, stream);

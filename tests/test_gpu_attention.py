@@ -261,7 +261,7 @@ def test_attention(bits, D, heads, G, page, ctx, draft, tree):
 
 @pytest.mark.parametrize("bits", BITS)
 @pytest.mark.parametrize("ctx,draft,G", [([2000, 1], [1, 1], 1), ([1500, 40, 333], [3, 20, 9], 4),
-                                         ([900], [64], 2)])
+                                         ([900], [64], 2), ([1100, 5], [70, 100], 4)])
 def test_attention_split_over_the_context(bits, ctx, draft, G):
     """A large hint splits the cached tokens over many CTAs, more than some
     sequences have tiles; with no hint there is one.  Both are right."""
@@ -284,7 +284,7 @@ def test_attention_rows_that_see_nothing(bits, hint):
 
 
 @pytest.mark.parametrize("bits", BITS)
-@pytest.mark.parametrize("draft", [3, 24])
+@pytest.mark.parametrize("draft", [3, 24, 70])
 def test_unseen_rows_have_no_influence(bits, draft):
     """Infinities, NaN and the types' largest values in the rest of a page, in
     pages of nobody and in drafted tokens that a row does not see; the rows that
@@ -311,9 +311,10 @@ def test_unseen_rows_have_no_influence(bits, draft):
         assert not torch.isfinite(out[dev(seen)].float()).any()
 
 
-def test_seen_infinity_in_fp16_values():
+@pytest.mark.parametrize("draft", [8, 15, 90])
+def test_seen_infinity_in_fp16_values(draft):
     """An infinity in a value that some rows see: those rows get it, in its channel only."""
-    c = Case(16, 64, 1, 1, 16, [20], [8], True, seed=9)
+    c = Case(16, 64, 1, 1, 16, [20], [draft], True, seed=9)
     pos = 20 + 2
     c.cache.v[int(c.table[0, pos // 16]), 0, pos % 16, 5] = float("inf")
     seen = torch.from_numpy((c.mask[:, 0] >> 2) & 1 > 0)
@@ -321,6 +322,9 @@ def test_seen_infinity_in_fp16_values():
     checked()
     assert torch.isinf(out[seen, :, 5]).all() and torch.isfinite(out[~seen]).all()
     assert torch.isfinite(out[seen][..., :5]).all() and torch.isfinite(out[seen][..., 6:]).all()
+    o, _, bo, _ = c.reference()
+    rest = [i for i in range(64) if i != 5]
+    within(out[..., rest], o[..., rest], bo[..., rest])
 
 
 @pytest.mark.parametrize("bits", BITS)
