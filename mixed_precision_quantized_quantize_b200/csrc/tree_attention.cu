@@ -1178,6 +1178,56 @@ __global__ void __launch_bounds__(128) tree_attention_join_kernel(const Params p
         p.lse[row] = L == 0.0f ? -INFINITY : (M - kShift + log2f(L)) * 0.693147180559945f;
 }
 
+// The same for up to four splits: a warp a row, every split's load in flight.
+template <int D>
+__global__ void __launch_bounds__(256) tree_attention_join4_kernel(const Params p) {
+    const int lane = threadIdx.x % 32;
+    const int h = blockIdx.y, b = blockIdx.z;
+    const Seq sq = sequence(p, b, false);  // (not written by the kernel that is waited for)
+    const int g = blockIdx.x * 8 + threadIdx.x / 32;
+    ptx::grid_dependency_wait();
+    if (g >= sq.n * p.group) return;
+    const int head = h * p.group + g % p.group, token = sq.first + g / p.group;
+    const int64_t row = static_cast<int64_t>(token) * p.q_heads + head;
+    const int64_t step = static_cast<int64_t>(p.tokens) * p.q_heads;
+    constexpr int V = D / 32;
+    float2 a[4];
+    float x[4][V];
+    float M = -INFINITY;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        const bool ok = s < p.splits;
+        a[s] = ok ? p.part_ml[s * step + row] : make_float2(-INFINITY, 0.0f);
+        const float *src = p.part_o + (s * step + row) * D + lane * V;
+        if constexpr (V == 4) {
+            const float4 v = ok ? *reinterpret_cast<const float4 *>(src) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            x[s][0] = v.x, x[s][1] = v.y, x[s][2] = v.z, x[s][3] = v.w;
+        } else {
+            const float2 v = ok ? *reinterpret_cast<const float2 *>(src) : make_float2(0.0f, 0.0f);
+            x[s][0] = v.x, x[s][1] = v.y;
+        }
+        M = fmaxf(M, a[s].x);
+    }
+    const float base = M == -INFINITY ? 0.0f : M;
+    float L = 0.0f, acc[V] = {};
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        const float f = exp2_fast(a[s].x - base);
+        L = fmaf(f, a[s].y, L);
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = fmaf(f, x[s][i], acc[i]);
+    }
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    uint16_t *dst = p.out + static_cast<int64_t>(token) * p.out_stride + head * D + lane * V;
+    if constexpr (V == 4)
+        *reinterpret_cast<uint2 *>(dst) =
+            make_uint2(half2_of(acc[0] * inv, acc[1] * inv), half2_of(acc[2] * inv, acc[3] * inv));
+    else
+        *reinterpret_cast<uint32_t *>(dst) = half2_of(acc[0] * inv, acc[1] * inv);
+    if (lane == 0 && p.lse != nullptr)
+        p.lse[row] = L == 0.0f ? -INFINITY : (M - kShift + log2f(L)) * 0.693147180559945f;
+}
+
 // ------------------------------------------------------------------ host side
 struct Plan {
     int wide;         // > 0: the tcgen05 form, with so many blocks of 128 rows a CTA
@@ -1247,9 +1297,11 @@ size_t partial_bytes(const AttentionArgs &a, const Plan &r) {
 
 // The join of a call's partial results, launched while the first kernel runs;
 // it waits for that kernel's results.
-quik_status launch_join(const Params &p, void (*kernel)(Params), int threads, cudaStream_t stream) {
+quik_status launch_join(const Params &p, void (*kernel)(Params), int threads, cudaStream_t stream,
+                        unsigned rows_a_block = 1) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.max_tokens) * p.group, p.heads, p.sequences);
+    const unsigned rows = static_cast<unsigned>(p.max_tokens) * p.group;
+    cfg.gridDim = dim3((rows + rows_a_block - 1) / rows_a_block, p.heads, p.sequences);
     cfg.blockDim = dim3(threads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -1258,6 +1310,12 @@ quik_status launch_join(const Params &p, void (*kernel)(Params), int threads, cu
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? QUIK_OK : QUIK_ERR_CUDA;
+}
+
+template <int D>
+quik_status join_splits(const Params &p, cudaStream_t stream) {
+    if (p.splits <= 4) return launch_join(p, &tree_attention_join4_kernel<D>, 256, stream, 8);
+    return launch_join(p, &tree_attention_join_kernel<D>, 128, stream);
 }
 
 template <class C>
@@ -1275,7 +1333,7 @@ quik_status run(const Params &p, void (*kernel)(Params), cudaStream_t stream) {
     const dim3 grid(p.splits * p.row_blocks, p.heads, p.sequences);
     kernel<<<grid, C::NW * 32, C::SMEM, stream>>>(p);
     if (p.splits > 1) {
-        const quik_status st = launch_join(p, &tree_attention_join_kernel<C::D>, 128, stream);
+        const quik_status st = join_splits<C::D>(p, stream);
         if (st != QUIK_OK) return st;
     }
     return cudaGetLastError() == cudaSuccess ? QUIK_OK : QUIK_ERR_CUDA;
@@ -1338,8 +1396,7 @@ quik_status launch_tree_attention(const AttentionArgs &a, cudaStream_t stream) {
     if (plan.wide > 0) {
         const quik_status st = launch_attention_wide(p, a.cache.kv_type, a.cache.head_dim, plan.wide, stream);
         if (st != QUIK_OK || p.splits == 1) return st;
-        return launch_join(p, a.cache.head_dim == 64 ? &tree_attention_join_kernel<64> : &tree_attention_join_kernel<128>,
-                           128, stream);
+        return a.cache.head_dim == 64 ? join_splits<64>(p, stream) : join_splits<128>(p, stream);
     }
     if (a.cache.kv_type == QUIK_KV_INT4) return run_dim<4>(p, a.cache.head_dim, plan.wr, stream);
     if (a.cache.kv_type == QUIK_KV_INT8) return run_dim<8>(p, a.cache.head_dim, plan.wr, stream);

@@ -14,8 +14,8 @@
 // S is double-buffered, so the products of tile t + 1 run under the softmax of
 // tile t, and the two row blocks' softmaxes under each other's products.
 //
-// The running maximum is only moved when a row's scores exceed it by 3 in log2
-// (p carries 2^12 here, so p <= 2^15 < 65504): rescaling O is a trip through
+// The running maximum is only moved when a row's scores exceed it by 5 in log2
+// (p carries 2^10 here, so p <= 2^15 < 65504): rescaling O is a trip through
 // tensor memory, and after the first tiles it hardly ever happens.
 //
 // Bound by the exponentials: 256 rows x 64 tokens take the 4 x 4 lanes of an
@@ -30,8 +30,8 @@ static __device__ unsigned int g_wide_waits;
 namespace {
 
 constexpr int kTok = 64;            // cached tokens per tile
-constexpr float kLazy = 3.0f;        // how far scores may pass the running maximum (log2)
-constexpr float kWideShift = 12.0f;  // p carries 2^12
+constexpr float kLazy = 5.0f;        // how far scores may pass the running maximum (log2)
+constexpr float kWideShift = 10.0f;  // p carries 2^10
 constexpr float kJoinShift = 14.0f;  // what the join takes p to carry
 constexpr int kLoaders = 128;
 
@@ -100,6 +100,13 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t addr, uint32_t block_bytes)
            ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // 16-byte chunk c (8 channels) of row r of an operand of `rows` rows.
 __device__ __forceinline__ uint32_t swizzled(int r, int c, int rows) {
     return (c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
@@ -120,7 +127,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (ptx::smem_u32(smem_raw) & 1023)) & 1023);
     WideBars *bars = reinterpret_cast<WideBars *>(smem + C::OFF_BAR);
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    // (values broadcast from lane 0 are the same in the whole warp for the compiler
+    // too: the products' descriptors and loop then live in uniform registers)
+    const int lane = threadIdx.x % 32, warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);
     const int split = blockIdx.x % p.splits, rb = blockIdx.x / p.splits;
     const int h = blockIdx.y, b = blockIdx.z;
     const Seq sq = sequence(p, b, blockIdx.x == 0 && h == 0 && threadIdx.x == 0);
@@ -128,7 +137,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
     if (row0 >= rows) return;
     const int tiles = (sq.total + kTok - 1) / kTok;
     const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * split / p.splits);
-    const int n = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / p.splits) - t0;
+    const int n = __shfl_sync(
+        0xffffffffu, static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / p.splits) - t0, 0);
 
     constexpr int MMA_WARP = QT * 4 + kLoaders / 32;
     if (threadIdx.x == 0) {
@@ -161,7 +171,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    const uint32_t tmem = bars->tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem, 0);
     volatile int *abort = &bars->abort;
     const auto s_col = [&](int g, int buf) { return tmem + (g * 2 + buf) * kTok; };
     const auto o_col = [&](int g) { return tmem + QT * 2 * kTok + g * D; };
@@ -599,22 +609,27 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
         copy_wait<0>();
     } else {
         // ================================================ products
+        // (descriptors are sums of a base and constants: in the low word, whose
+        // address field does not overflow below 256 KB)
         const uint32_t base = ptx::smem_u32(smem);
         constexpr uint32_t id_s = ptx::idesc_f16_f32(128, kTok), id_o = ptx::idesc_f16_f32(128, D) | (1u << 16);
+        const uint64_t dq = ptx::sw128_kmajor_desc(base), dk = ptx::sw128_kmajor_desc(base + C::OFF_KV);
+        const uint64_t dv = mn_desc(base + C::OFF_KV + C::HALF, kTok * 128);
+        const bool leader = elect_one();
         auto pv = [&](int t) {  // O += P V of tile t, both row blocks
             const int stage = t % C::STAGES, buf = t & 1;
-            const uint32_t v = base + C::OFF_KV + stage * 2 * C::HALF + C::HALF;
+            const uint64_t v = dv + static_cast<uint32_t>(stage * (2 * C::HALF / 16));
+#pragma unroll
             for (int g = 0; g < QT; ++g) {
                 if (!wide_wait(&bars->p_full[g][buf], (t >> 1) & 1, abort)) return false;
                 ptx::tc_fence_after();
-                if (lane == 0) {
+                if (leader) {
 #pragma unroll
                     for (int k = 0; k < kTok / 16; ++k)
-                        mma_f16_ts(o_col(g), s_col(g, buf) + 8 * k, mn_desc(v + k * 2048, kTok * 128), id_o);
+                        mma_f16_ts(o_col(g), s_col(g, buf) + 8 * k, v + k * (2048 / 16), id_o);
                     ptx::mma_commit(&bars->pv_done[g]);
                     if (g == QT - 1) ptx::mma_commit(&bars->kv_empty[stage]);
                 }
-                __syncwarp();
             }
             return true;
         };
@@ -624,24 +639,23 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
             alive = wide_wait(&bars->kv_full[stage], (t / C::STAGES) & 1, abort);
             if (!alive) break;
             ptx::tc_fence_after();
-            if (lane == 0) {
-                const uint32_t k = base + C::OFF_KV + stage * 2 * C::HALF;
+            if (leader) {
+                const uint64_t k = dk + static_cast<uint32_t>(stage * (2 * C::HALF / 16));
+#pragma unroll
                 for (int g = 0; g < QT; ++g) {
 #pragma unroll
                     for (int i = 0; i < C::STEPS; ++i)
-                        ptx::mma_f16(s_col(g, buf),
-                                     ptx::sw128_kmajor_desc(base + g * (128 * D * 2) + i / 4 * 16384 + i % 4 * 32),
-                                     ptx::sw128_kmajor_desc(k + i / 4 * (kTok * 128) + i % 4 * 32), id_s, i > 0);
+                        ptx::mma_f16(s_col(g, buf), dq + (g * (128 * D * 2) + i / 4 * 16384 + i % 4 * 32) / 16,
+                                     k + (i / 4 * (kTok * 128) + i % 4 * 32) / 16, id_s, i > 0);
                     ptx::mma_commit(&bars->s_full[g][buf]);
                 }
             }
-            __syncwarp();
             if (t > 0) alive = pv(t - 1);
             if (!alive) break;
         }
         if (alive && n > 0) pv(n - 1);
         // whatever was issued has to end before its memory is given back
-        if (lane == 0) ptx::mma_commit(&bars->drain);
+        if (leader) ptx::mma_commit(&bars->drain);
         __syncwarp();
         int none = 0;
         wide_wait(&bars->drain, 0, &none);

@@ -123,14 +123,14 @@ def attention(q, K, V, page_size, table, context, cu, mask, scale):
                 size = p @ np.abs(v)
                 # p: half a step of fp16, its score's error twice (p and the sum),
                 # the products' fp32 sums; the result: half a step.  A p far below the
-                # largest is a subnormal: carrying 2^12 or more, and the quantised
+                # largest is a subnormal: carrying 2^10 or more, and the quantised
                 # values' scale over a power of two at most four times the largest
                 # scale among the sequence's rows, it is off by at most
-                # 2^-25 2^-12 4 max|v| a token, over the sum of the e's
+                # 2^-25 2^-10 4 max|v| a token, over the sum of the e's
                 most = np.abs(V[pg, h // G, pos % page_size]).max()
                 b_out[row, h] = (size * (HALF_F16 + 2 * d + (len(s) + 8) * 2.0 ** -23) * (1 + HALF_F16)
                                  + HALF_F16 * np.abs(out[row, h]) + TINY_F16
-                                 + len(s) * most * 2.0 ** -35 / z)
+                                 + len(s) * most * 2.0 ** -33 / z)
                 b_lse[row, h] = d + (len(s) + 8) * 2.0 ** -24 + abs(lse[row, h]) * 2.0 ** -22 + abs(m) * 2.0 ** -22
     return out, lse, b_out, b_lse
 
