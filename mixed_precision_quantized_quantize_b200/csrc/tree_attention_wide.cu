@@ -6,7 +6,7 @@
 //     S = Q K^T    tcgen05 kind::f16, 128 x 64, both operands in shared memory
 //     p            four warps a row block, a thread a row, as in tree_attention.cu
 //     O += P V     P in tensor memory (over the S it came from), V in shared memory
-// Four loader warps bring the cached rows in by cp.async; quantised rows land in
+// Three loader warps bring the cached rows in by cp.async; quantised rows land in
 // a raw ring and are converted to fp16 (exact: they are integer codes) into the
 // products' operand tiles, once for both row blocks.  K and V tiles have one
 // image, [64 tokens][64 channels] blocks in the 128-byte swizzle: K is read
@@ -33,7 +33,7 @@ constexpr int kTok = 64;            // cached tokens per tile
 constexpr float kLazy = 5.0f;        // how far scores may pass the running maximum (log2)
 constexpr float kWideShift = 10.0f;  // p carries 2^10
 constexpr float kJoinShift = 14.0f;  // what the join takes p to carry
-constexpr int kLoaders = 128;
+constexpr int kLoaders = 96;     // 12 warps in all with two row blocks: 168 registers a thread
 
 template <int BITS_, int D_, int QT_>
 struct WideCfg {
@@ -45,7 +45,7 @@ struct WideCfg {
     static constexpr int STAGES = BITS == 16 ? 4 : 3;
     static constexpr int RAW = BITS == 16 ? 0 : 2 * kTok * RB + 2 * kTok * 4;
     static constexpr int RAWS = BITS == 16 ? 0 : BITS == 8 ? 3 : 4;
-    static constexpr int META = 2 * kTok * 4 + 64;  // K scales, V scales, int4, 4 x int2
+    static constexpr int META = 2 * kTok * 4 + 64;  // K scales, V scales, int4, an int2 of each loader warp
     static constexpr int OFF_KV = Q_BYTES;
     static constexpr int OFF_RAW = OFF_KV + STAGES * 2 * HALF;
     static constexpr int OFF_META = OFF_RAW + RAWS * RAW;
@@ -62,25 +62,26 @@ struct WideBars {
     int abort;
 };
 
-// Wait for a phase, for at most kWaitLimitNs and not once another role has
-// given up.  The whole warp takes part and gets one answer.
-__device__ __forceinline__ bool wide_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    bool ok = ptx::mbar_try_wait(bar, parity);
-    if (!__all_sync(0xffffffffu, ok)) {
-        const uint64_t t0 = ptx::global_timer_ns();
-        while (!ok) {
-            ok = ptx::mbar_try_wait(bar, parity);
-            if (ok || *abort) break;
-            if (ptx::global_timer_ns() - t0 > kWaitLimitNs) {
-                *abort = 1;
-                atomicAdd(&g_wide_waits, 1u);
-                break;
-            }
+// Wait for a phase, for at most kWaitLimitNs and not once another role has given
+// up.  Every lane of a warp waits for itself; a warp goes by all_of its answers.
+__device__ __noinline__ bool wide_wait_slowly(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    const uint64_t t0 = ptx::global_timer_ns();
+    while (true) {
+        if (ptx::mbar_try_wait(bar, parity)) return true;
+        if (*abort) return false;
+        if (ptx::global_timer_ns() - t0 > kWaitLimitNs) {
+            *abort = 1;
+            atomicAdd(&g_wide_waits, 1u);
+            return false;
         }
-        __syncwarp();
     }
-    return __all_sync(0xffffffffu, ok);
 }
+__device__ __forceinline__ bool wide_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    for (int i = 0; i < 4; ++i)
+        if (ptx::mbar_try_wait(bar, parity)) return true;
+    return wide_wait_slowly(bar, parity, abort);
+}
+__device__ __forceinline__ bool all_of(bool ok) { return __all_sync(0xffffffffu, ok); }
 
 // D[tmem] += A[tmem] * B[smem desc], fp16 kind, A in tensor memory (lane = row,
 // two fp16 a column, K in column order).
@@ -196,8 +197,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
             const int stage = t % C::STAGES, buf = t & 1;
             const uint8_t *meta = smem + C::OFF_META + stage * C::META;
             // (the tile's scales and masks come from the loaders, S from the products)
-            alive = wide_wait(&bars->kv_full[stage], (t / C::STAGES) & 1, abort) &&
-                    wide_wait(&bars->s_full[g][buf], (t >> 1) & 1, abort);
+            alive = all_of(wide_wait(&bars->kv_full[stage], (t / C::STAGES) & 1, abort) &&
+                           wide_wait(&bars->s_full[g][buf], (t >> 1) & 1, abort));
             if (!alive) break;
             ptx::tc_fence_after();
             uint32_t s[64];
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
                 if (unit != R) alpha *= exp2_fast(static_cast<float>(R - unit));
                 R = unit;
                 if (t > 0) {  // (O is zero before the first tile)
-                    alive = wide_wait(&bars->pv_done[g], (t - 1) & 1, abort);
+                    alive = all_of(wide_wait(&bars->pv_done[g], (t - 1) & 1, abort));
                     if (!alive) break;
                     ptx::tc_fence_after();
 #pragma unroll
@@ -302,10 +303,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
                 // rows that see the token add them here
                 const uint4 w0 = *reinterpret_cast<const uint4 *>(meta + 2 * kTok * 4 + 16);
                 const uint4 w1 = *reinterpret_cast<const uint4 *>(meta + 2 * kTok * 4 + 32);
-                const unsigned odds[2] = {w0.x | w0.z | w1.x | w1.z, w0.y | w0.w | w1.y | w1.w};
+                const unsigned odds[2] = {w0.x | w0.z | w1.x, w0.y | w0.w | w1.y};  // of three warps
                 if ((odds[0] | odds[1]) != 0) {
                     if (t > 0) {
-                        alive = wide_wait(&bars->pv_done[g], (t - 1) & 1, abort);
+                        alive = all_of(wide_wait(&bars->pv_done[g], (t - 1) & 1, abort));
                         if (!alive) break;
                         ptx::tc_fence_after();
                     }
@@ -356,7 +357,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
             ptx::tc_fence_before();
             ptx::mbar_arrive(&bars->p_full[g][buf]);
         }
-        if (alive && n > 0) alive = wide_wait(&bars->pv_done[g], (n - 1) & 1, abort);
+        if (alive && n > 0) alive = all_of(wide_wait(&bars->pv_done[g], (n - 1) & 1, abort));
         if (alive) {
             // ---- results, 16 channels at a time through shared memory (Q's place:
             // every product that reads it is done) into whole lines
@@ -419,8 +420,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
     } else if (warp < MMA_WARP) {
         // ================================================ loaders
         const int lt = threadIdx.x - QT * 128;
-        constexpr int PER = kTok * C::CPR / kLoaders > 0 ? kTok * C::CPR / kLoaders : 1;  // chunks of K a thread
-        constexpr int TSTEP = kLoaders / C::CPR;  // tokens from one of them to the next
+        // a thread's chunks of K (and V): the same place in rows TSTEP apart
+        constexpr int CHUNKS = kTok * C::CPR, PER = (CHUNKS + kLoaders - 1) / kLoaders;
+        constexpr int TSTEP = kLoaders / C::CPR;
+        static_assert(kLoaders % C::CPR == 0, "a thread keeps its place in the rows");
         const int tok0 = lt / C::CPR, ch = lt % C::CPR;
         const int32_t *table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
         const int64_t head = static_cast<int64_t>(h) << p.page_shift;
@@ -451,12 +454,25 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
             const unsigned in = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
             return in & ((id[2 * half] >= 0 ? 0xffffu : 0u) | (id[2 * half + 1] >= 0 ? 0xffff0000u : 0u));
         };
-        // copies of a tile's rows (dst: this thread's chunk of the K rows, V at v_off from it)
+        // copies of a tile's rows, to where dst_of(token, 0 or 1 for V) says
         auto copies = [&](int t, const int (&id)[4], auto dst_of) {
+            const bool whole = (t0 + t + 1) * kTok <= sq.total && (id[0] | id[1] | id[2] | id[3]) >= 0;
+            if (whole && p.page_shift >= 6) {
+                // in one page, and there: one offset places it all
+                const int64_t off = row_of(id[0], t, 0) * C::RB + lt * 16;
+                const uint8_t *k = p.k + off, *v = p.v + off;
+#pragma unroll
+                for (int j = 0; j < PER; ++j) {
+                    if (CHUNKS % kLoaders != 0 && lt + j * kLoaders >= CHUNKS) break;
+                    copy16(dst_of(tok0 + j * TSTEP, 0), k + j * kLoaders * 16, true);
+                    copy16(dst_of(tok0 + j * TSTEP, 1), v + j * kLoaders * 16, true);
+                }
+                return;
+            }
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
                 const int token = tok0 + j * TSTEP;
-                if (kTok * C::CPR < kLoaders && token >= kTok) break;
+                if (CHUNKS % kLoaders != 0 && lt + j * kLoaders >= CHUNKS) break;
                 const int pid = id_of(id, token / 16);
                 const bool ok = pid >= 0 && (t0 + t) * kTok + token < sq.total;
                 const int64_t off = ok ? row_of(pid, t, token) * C::RB + ch * 16 : 0;
@@ -479,7 +495,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
                 if (t < n) {
                     const int stage = t % C::STAGES;
                     if (t >= C::STAGES)
-                        alive = wide_wait(&bars->kv_empty[stage], (t / C::STAGES - 1) & 1, abort);
+                        alive = all_of(wide_wait(&bars->kv_empty[stage], (t / C::STAGES - 1) & 1, abort));
                     if (!alive) break;
                     const uint32_t at = ptx::smem_u32(smem) + C::OFF_KV + stage * 2 * C::HALF;
                     copies(t, id, [&](int token, int v) { return at + v * C::HALF + swizzled(token, ch, kTok); });
@@ -503,6 +519,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
 #pragma unroll
                     for (int j = 0; j < PER; ++j) {
                         const int token = tok0 + j * TSTEP;
+                        if (CHUNKS % kLoaders != 0 && lt + j * kLoaders >= CHUNKS) break;
                         uint4 *at = reinterpret_cast<uint4 *>(v + swizzled(token, ch, kTok));
                         if (not_finite(*at)) {
                             *at = make_uint4(0, 0, 0, 0);
@@ -524,7 +541,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
                 if (t < n) {
                     uint8_t *raw = raws + t % C::RAWS * C::RAW;
                     const uint32_t at = ptx::smem_u32(raw);
-                    copies(t, id, [&](int token, int v) { return at + v * kTok * C::RB + token * C::RB + ch * 16; });
+                    copies(t, id, [&](int token, int v) { return at + (v * kTok + token) * C::RB + ch * 16; });
                     if (lt < 32) {
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
@@ -548,13 +565,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
                 pages(t + 1, id);
             }
             for (int t = 0; t < n; ++t) {
-                issue(t + C::RAWS - 1);
-                live[C::RAWS - 1][0] = live_of(id, t + C::RAWS - 1, 0);
-                live[C::RAWS - 1][1] = live_of(id, t + C::RAWS - 1, 1);
-                pages(t + C::RAWS, id);
-                copy_wait<C::RAWS - 1>();
+                copy_wait<C::RAWS - 2>();
                 const int stage = t % C::STAGES;
-                if (t >= C::STAGES && !wide_wait(&bars->kv_empty[stage], (t / C::STAGES - 1) & 1, abort)) break;
+                if (t >= C::STAGES && !all_of(wide_wait(&bars->kv_empty[stage], (t / C::STAGES - 1) & 1, abort))) break;
                 const uint8_t *raw = raws + t % C::RAWS * C::RAW;
                 uint8_t *kv = smem + C::OFF_KV + stage * 2 * C::HALF;
                 uint8_t *meta = smem + C::OFF_META + stage * C::META;
@@ -572,38 +585,51 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
                             make_int4(static_cast<int>(live[0][0]), static_cast<int>(live[0][1]),
                                       (t0 + t) * kTok - sq.ctx, R);
                 }
+                // this thread's own chunks, from codes to fp16: K's, then V's (loads first,
+                // which the compiler cannot move over the stores)
 #pragma unroll
-                for (int i = 0; i < C::RAWS - 1; ++i) live[i][0] = live[i + 1][0], live[i][1] = live[i + 1][1];
-                // this thread's own chunks, from codes to fp16
+                for (int v = 0; v < 2; ++v) {
+                    uint4 w4[PER];
 #pragma unroll
-                for (int j = 0; j < 2 * PER; ++j) {
-                    const int token = tok0 + j / 2 * TSTEP, v = j & 1;
-                    if (kTok * C::CPR < kLoaders && token >= kTok) break;
-                    const uint4 w4 = *reinterpret_cast<const uint4 *>(raw + v * kTok * C::RB + token * C::RB + ch * 16);
-                    const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-                    uint8_t *dst = kv + v * C::HALF;
-                    if constexpr (BITS == 8) {
+                    for (int j = 0; j < PER; ++j)
+                        if (CHUNKS % kLoaders == 0 || lt + j * kLoaders < CHUNKS)
+                            w4[j] = *reinterpret_cast<const uint4 *>(raw + v * kTok * C::RB + (lt + j * kLoaders) * 16);
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint32_t a = w[2 * i] ^ 0x80808080u, c = w[2 * i + 1] ^ 0x80808080u;
-                            *reinterpret_cast<uint4 *>(dst + swizzled(token, 2 * ch + i, kTok)) =
-                                make_uint4(pair8(a, false), pair8(a, true), pair8(c, false), pair8(c, true));
-                        }
-                    } else {
+                    for (int j = 0; j < PER; ++j) {
+                        if (CHUNKS % kLoaders != 0 && lt + j * kLoaders >= CHUNKS) break;
+                        const int token = tok0 + j * TSTEP;
+                        const uint32_t w[4] = {w4[j].x, w4[j].y, w4[j].z, w4[j].w};
+                        uint8_t *dst = kv + v * C::HALF;
+                        if constexpr (BITS == 8) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            // pairs (0, 4), (1, 5), (2, 6), (3, 7) into channel order
-                            const uint32_t y = w[i] >> 8;
-                            const uint32_t a = pair4(w[i], false), c = pair4(w[i], true), d = pair4(y, false),
-                                           f = pair4(y, true);
-                            *reinterpret_cast<uint4 *>(dst + swizzled(token, 4 * ch + i, kTok)) =
-                                make_uint4(pick(a, c, 0x5410u), pick(d, f, 0x5410u), pick(a, c, 0x7632u),
-                                           pick(d, f, 0x7632u));
+                            for (int i = 0; i < 2; ++i) {
+                                const uint32_t a = w[2 * i] ^ 0x80808080u, c = w[2 * i + 1] ^ 0x80808080u;
+                                *reinterpret_cast<uint4 *>(dst + swizzled(token, 2 * ch + i, kTok)) =
+                                    make_uint4(pair8(a, false), pair8(a, true), pair8(c, false), pair8(c, true));
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                // pairs (0, 4), (1, 5), (2, 6), (3, 7) into channel order
+                                const uint32_t y = w[i] >> 8;
+                                const uint32_t a = pair4(w[i], false), c = pair4(w[i], true), d = pair4(y, false),
+                                               f = pair4(y, true);
+                                *reinterpret_cast<uint4 *>(dst + swizzled(token, 4 * ch + i, kTok)) =
+                                    make_uint4(pick(a, c, 0x5410u), pick(d, f, 0x5410u), pick(a, c, 0x7632u),
+                                               pick(d, f, 0x7632u));
+                            }
                         }
                     }
                 }
                 ptx::fence_proxy_async_smem();
                 ptx::mbar_arrive(&bars->kv_full[stage]);
+                // the raw slot of the tile before this one is free: refill it
+                issue(t + C::RAWS - 1);
+                live[C::RAWS - 1][0] = live_of(id, t + C::RAWS - 1, 0);
+                live[C::RAWS - 1][1] = live_of(id, t + C::RAWS - 1, 1);
+                pages(t + C::RAWS, id);
+#pragma unroll
+                for (int i = 0; i < C::RAWS - 1; ++i) live[i][0] = live[i + 1][0], live[i][1] = live[i + 1][1];
             }
         }
         copy_wait<0>();
@@ -621,7 +647,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
             const uint64_t v = dv + static_cast<uint32_t>(stage * (2 * C::HALF / 16));
 #pragma unroll
             for (int g = 0; g < QT; ++g) {
-                if (!wide_wait(&bars->p_full[g][buf], (t >> 1) & 1, abort)) return false;
+                if (!all_of(wide_wait(&bars->p_full[g][buf], (t >> 1) & 1, abort))) return false;
                 ptx::tc_fence_after();
                 if (leader) {
 #pragma unroll
@@ -636,7 +662,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
         bool alive = true;
         for (int t = 0; t < n; ++t) {
             const int stage = t % C::STAGES, buf = t & 1;
-            alive = wide_wait(&bars->kv_full[stage], (t / C::STAGES) & 1, abort);
+            alive = all_of(wide_wait(&bars->kv_full[stage], (t / C::STAGES) & 1, abort));
             if (!alive) break;
             ptx::tc_fence_after();
             if (leader) {
