@@ -57,7 +57,7 @@ struct WideCfg {
 };
 
 struct WideBars {
-    uint64_t kv_full[4], kv_empty[4], s_full[2][2], p_full[2][2], pv_done[2], drain;
+    uint64_t kv_full[4], kv_empty[4], s_full[2][2], p_full[2][2], pv_done[2], q_full, drain;
     uint32_t tmem;
     int abort;
 };
@@ -154,21 +154,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
             }
             ptx::mbar_init(&bars->pv_done[g], 1);
         }
+        ptx::mbar_init(&bars->q_full, QT * 128);
         ptx::mbar_init(&bars->drain, 1);
         bars->abort = 0;
         ptx::fence_barrier_init();
     }
     if (warp == MMA_WARP) ptx::tmem_alloc(&bars->tmem, C::ALLOC);
-    // ---- Q, rows past the last as zeros
-    for (int x = threadIdx.x; x < QT * 128 * (D / 8); x += C::THREADS) {
-        const int r = x / (D / 8), c = x % (D / 8), g = row0 + r;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (g < rows)
-            v = *reinterpret_cast<const uint4 *>(p.q + static_cast<int64_t>(sq.first + g / p.group) * p.q_stride +
-                                                 static_cast<int64_t>(h * p.group + g % p.group) * D + 8 * c);
-        *reinterpret_cast<uint4 *>(smem + r / 128 * (128 * D * 2) + swizzled(r % 128, c, 128)) = v;
-    }
-    ptx::fence_proxy_async_smem();
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -186,11 +177,23 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
         float m = -INFINITY, l = 0.0f;
         int R = -100;
         {
+            // this row of Q (zeros past the last)
+            const uint16_t *src = p.q;
+            if (tok >= 0)
+                src += static_cast<int64_t>(sq.first + tok) * p.q_stride +
+                       static_cast<int64_t>(h * p.group + row % p.group) * D;
+            const uint32_t dst = ptx::smem_u32(smem) + g * (128 * D * 2);
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) copy16(dst + swizzled((warp % 4) * 32 + lane, c, 128), src + 8 * c, tok >= 0);
+            copy_commit();
             uint32_t z[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) z[i] = 0;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) ptx::tmem_st_32x32b_x32(o_col(g) + lanes + 32 * c, z);
+            copy_wait<0>();
+            ptx::fence_proxy_async_smem();
+            ptx::mbar_arrive(&bars->q_full);
         }
         bool alive = true;
         for (int t = 0; t < n; ++t) {
@@ -376,6 +379,22 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
                 else if (p.lse != nullptr)
                     p.lse[at] = l == 0.0f ? -INFINITY : (m - kWideShift + log2f(l)) * 0.693147180559945f;
             }
+            // where this lane writes: four rows of partial results, or two of the output
+            float *part[4];
+            uint16_t *out[2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int q = first_row + (p.splits > 1 ? i * 8 + lane / 4 : i * 16 + lane / 2);
+                const int64_t token = sq.first + q / p.group, head = h * p.group + q % p.group;
+                part[i] = nullptr;
+                if (i < 2) out[i] = nullptr;
+                if (q >= rows) continue;
+                if (p.splits > 1)
+                    part[i] = p.part_o + ((static_cast<int64_t>(split) * p.tokens + token) * p.q_heads + head) * D +
+                              lane % 4 * 4;
+                else if (i < 2)
+                    out[i] = p.out + token * p.out_stride + head * D + lane % 2 * 8;
+            }
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
                 uint32_t o[16];
@@ -389,29 +408,19 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
                 __syncwarp();
                 if (p.splits > 1) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = i * 8 + lane / 4, q = first_row + r;
-                        if (q < rows) {
-                            const int64_t at = static_cast<int64_t>(split) * p.tokens * p.q_heads +
-                                               static_cast<int64_t>(sq.first + q / p.group) * p.q_heads +
-                                               h * p.group + q % p.group;
-                            *reinterpret_cast<float4 *>(p.part_o + at * D + 16 * c + lane % 4 * 4) =
-                                *reinterpret_cast<const float4 *>(buf + r * 20 + lane % 4 * 4);
-                        }
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        if (part[i] != nullptr)
+                            *reinterpret_cast<float4 *>(part[i] + 16 * c) =
+                                *reinterpret_cast<const float4 *>(buf + (i * 8 + lane / 4) * 20 + lane % 4 * 4);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const int r = i * 16 + lane / 2, q = first_row + r;
-                        if (q < rows) {
-                            const float4 x = *reinterpret_cast<const float4 *>(buf + r * 20 + lane % 2 * 8);
-                            const float4 y = *reinterpret_cast<const float4 *>(buf + r * 20 + lane % 2 * 8 + 4);
-                            *reinterpret_cast<uint4 *>(p.out +
-                                                       static_cast<int64_t>(sq.first + q / p.group) * p.out_stride +
-                                                       (h * p.group + q % p.group) * D + 16 * c + lane % 2 * 8) =
-                                make_uint4(half2_of(x.x, x.y), half2_of(x.z, x.w), half2_of(y.x, y.y),
-                                           half2_of(y.z, y.w));
-                        }
+                        if (out[i] == nullptr) continue;
+                        const float *r = buf + (i * 16 + lane / 2) * 20 + lane % 2 * 8;
+                        const float4 x = *reinterpret_cast<const float4 *>(r);
+                        const float4 y = *reinterpret_cast<const float4 *>(r + 4);
+                        *reinterpret_cast<uint4 *>(out[i] + 16 * c) =
+                            make_uint4(half2_of(x.x, x.y), half2_of(x.z, x.w), half2_of(y.x, y.y), half2_of(y.z, y.w));
                     }
                 }
                 __syncwarp();
@@ -659,8 +668,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
             }
             return true;
         };
-        bool alive = true;
-        for (int t = 0; t < n; ++t) {
+        bool alive = n == 0 || all_of(wide_wait(&bars->q_full, 0, abort));
+        for (int t = 0; t < n && alive; ++t) {
             const int stage = t % C::STAGES, buf = t & 1;
             alive = all_of(wide_wait(&bars->kv_full[stage], (t / C::STAGES) & 1, abort));
             if (!alive) break;
