@@ -25,7 +25,10 @@ using Params = AttnParams;
 constexpr int kTile = 32;          // cached tokens per tile
 constexpr float kShift = 14.0f;    // p carries 2^14
 constexpr int kMaxSplits = 64;
-constexpr int kWideRows = 64;      // more rows of a key head than this: the tcgen05 form
+// More rows of a key head than this: the tcgen05 form.  Over 4096 INT8 tokens
+// (8 sequences, 8 key heads) it takes 47-49 us whatever the rows up to 64, the
+// warp products 32 us with 16 rows, 47 with 32, 72 with 48.
+constexpr int kWideRows = 32;
 
 // WR warps share a tile, 16 rows each; NW / WR such groups take tiles in turn.
 template <int BITS_, int D_, int WR_, int NW_>
@@ -552,7 +555,7 @@ __global__ void __launch_bounds__(C::NW * 32) tree_attention_kernel(const Params
 // over INT4, of which 28 us remained without any arithmetic.)
 template <int BITS_, int D_>
 struct FewCfg {
-    static constexpr int BITS = BITS_, D = D_, WR = 1, NW = 4, ROWS = 8;
+    static constexpr int BITS = BITS_, D = D_, WR = 1, NW = 4;
     static constexpr int RB = D * BITS / 8, CPR = RB / 16;
     static constexpr int KS = RB >= 128 ? RB + 16 : RB, VS = RB + 16;
     static constexpr int SCALES = BITS == 16 ? 0 : 2 * kTile * 4;
@@ -1244,13 +1247,13 @@ int few_ctas(int head_dim) {
 // Up to eight rows: the transposed form (wr 0), with as many workers as are
 // resident at once, or one for each tile (a tile takes a lone warp more than a
 // microsecond: one token over 200, 32 heads: 11.8 us with four tiles a worker).
-// More rows: the fewest row warps that hold them (a warp's products have 16),
-// up to four, and splits of the cached tokens, enough CTAs for about two a
-// resident slot, while each warp group keeps at least four tiles.
+// Up to 32: one or two row warps (a warp's products have 16), and splits of the
+// cached tokens, enough CTAs for about two a resident slot, while each warp
+// group keeps at least four tiles.
 Plan plan_of(const AttentionArgs &a) {
     Plan r{};
     const int64_t rows = static_cast<int64_t>(a.max_tokens) * (a.q_heads / a.cache.heads);
-    r.wr = rows <= 8 ? 0 : rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+    r.wr = rows <= 8 ? 0 : rows <= 16 ? 1 : 2;
     const int block = r.wr == 0 ? 8 : 16 * r.wr;
     r.row_blocks = static_cast<int>((rows + block - 1) / block);
     const int64_t items = static_cast<int64_t>(a.sequences) * a.cache.heads * r.row_blocks;
@@ -1343,8 +1346,7 @@ template <int BITS, int D>
 quik_status run_rows(const Params &p, int wr, cudaStream_t stream) {
     if (wr == 0) return run_few<FewCfg<BITS, D>>(p, stream);
     if (wr == 1) return run<Cfg<BITS, D, 1, 4>>(p, &tree_attention_kernel<Cfg<BITS, D, 1, 4>>, stream);
-    if (wr == 2) return run<Cfg<BITS, D, 2, 4>>(p, &tree_attention_kernel<Cfg<BITS, D, 2, 4>>, stream);
-    return run<Cfg<BITS, D, 4, 4>>(p, &tree_attention_kernel<Cfg<BITS, D, 4, 4>>, stream);
+    return run<Cfg<BITS, D, 2, 4>>(p, &tree_attention_kernel<Cfg<BITS, D, 2, 4>>, stream);
 }
 
 template <int BITS>
