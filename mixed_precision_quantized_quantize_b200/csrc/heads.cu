@@ -2,18 +2,20 @@
 // the per-head RMS norm with the rotation (qk_norm_rope), the append of K and
 // V rows to the paged cache (kv_append) and the read-back (kv_gather).
 //
-// A row is one head of one token, D = 64 or 128 channels.  D / 8 lanes hold a
-// row, eight channels each, so a warp holds 4 or 2 rows and all reductions over
-// a row are shuffles inside that lane group.  A lane's eight channels are two
-// runs of four, placed so that both channels of every rotated pair are in the
-// same lane: with pairs (i, i + rotary_dim / 2) a run and the one rotary_dim / 2
-// further on, otherwise two adjacent runs.  The rotation then needs no exchange
-// between lanes.  (With 16-byte loads and the partner's channels shuffled in,
-// norm and rotation of 2048 x 64 heads took 18.6 us.)  The table entries of a
-// token are loaded once and serve all the rows that a warp takes of it.
+// A row is one head of one token, D = 64 or 128 channels.  In the first two
+// D / 16 lanes hold a row, sixteen channels each, so a warp holds 8 or 4 rows
+// and all reductions over a row are shuffles inside that lane group.  A lane's
+// channels are two runs of eight (16-byte loads), placed so that both channels
+// of every rotated pair are in the same lane: with pairs (i, i + rotary_dim / 2)
+// a run and the one rotary_dim / 2 further on, otherwise two adjacent runs.  The
+// rotation then needs no exchange between lanes.  The table entries of a token
+// are loaded once and serve all the rows that a warp takes of it.
 //
-// All three kernels are bound by memory: every channel is read once and
-// written once.
+// Every channel is read once and written once, but at these sizes the kernels
+// are bound by instructions as much as by memory, so the arithmetic is paired
+// (two fp32 an instruction).  Norm and rotation of 2048 x 64 heads: 18.6 us with
+// eight channels a lane and the partner's shuffled in, 15.3 us with two runs of
+// four.
 #include "quik_internal.h"
 #include "sm100.cuh"
 
@@ -34,29 +36,31 @@ using ptx::f2_mul;
 using ptx::f2_split;
 using ptx::f2_sub;
 
-__device__ __forceinline__ uint2 load8(const void *p) { return *reinterpret_cast<const uint2 *>(p); }
-__device__ __forceinline__ void store8(void *p, uint2 v) { *reinterpret_cast<uint2 *>(p) = v; }
+__device__ __forceinline__ uint4 load16(const void *p) { return *reinterpret_cast<const uint4 *>(p); }
+__device__ __forceinline__ void store16(void *p, uint4 v) { *reinterpret_cast<uint4 *>(p) = v; }
 
-// Four fp16 channels as two fp32 pairs, and back (rounded to nearest).
-__device__ __forceinline__ void unpack4(uint2 v, uint64_t *x) {
-    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&v.x));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&v.y));
-    x[0] = f2(a.x, a.y);
-    x[1] = f2(b.x, b.y);
+// Eight fp16 channels as four fp32 pairs, and back (rounded to nearest).
+__device__ __forceinline__ void unpack8(uint4 v, uint64_t *x) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+        x[i] = f2(f.x, f.y);
+    }
 }
-__device__ __forceinline__ uint2 pack4(const uint64_t *x) {
-    float a, b;
-    uint2 v;
-    f2_split(x[0], a, b);
-    __half2 h = __floats2half2_rn(a, b);
-    v.x = *reinterpret_cast<const uint32_t *>(&h);
-    f2_split(x[1], a, b);
-    h = __floats2half2_rn(a, b);
-    v.y = *reinterpret_cast<const uint32_t *>(&h);
-    return v;
+__device__ __forceinline__ uint4 pack8(const uint64_t *x) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a, b;
+        f2_split(x[i], a, b);
+        const __half2 h = __floats2half2_rn(a, b);
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A lane's channels: runs of four at a and b.
+// A lane's channels: runs of eight at a and b.
 struct Runs {
     int a, b;
 };
@@ -64,28 +68,33 @@ template <bool INTER>
 __device__ __forceinline__ Runs runs_of(int rotary, int i) {
     const int half = rotary / 2;
     Runs r;
-    if (!INTER && 4 * i < half) {
-        r.a = 4 * i;
-        r.b = half + 4 * i;
+    if (!INTER && 8 * i < half) {
+        r.a = 8 * i;
+        r.b = half + 8 * i;
     } else {
-        r.a = 8 * i;  // (half-split: the i-th run pair from rotary_dim on is at 2 * 4 i, too)
-        r.b = r.a + 4;
+        r.a = 16 * i;  // (half-split: lanes half / 8 on go on at rotary_dim)
+        r.b = r.a + 8;
     }
     return r;
 }
 
-// The rotation of one token, as this lane needs it: cosines and sines of its
-// four pairs.
+// The rotation of one token, as this lane needs it.  Half-split: cosines and
+// sines of its eight pairs, two a word; s is the run b's factor in run a, minus
+// the sine, n the run a's in run b.  Adjacent pairs: one angle a word, twice,
+// the sine with the sign of its channel.
+template <bool INTER>
 struct Turn {
-    float c[4], s[4];
-    bool on;  // this lane's channels are rotated
+    uint64_t c[INTER ? 8 : 4], s[INTER ? 8 : 4], n[INTER ? 1 : 4];
+    uint64_t zero;  // -0, -0, not known to the compiler
+    bool on;        // this lane's channels are rotated
 };
 
 template <bool INTER>
-__device__ __forceinline__ Turn load_turn(const RotaryArgs &r, int token, int i) {
-    Turn t;
+__device__ __forceinline__ Turn<INTER> load_turn(const RotaryArgs &r, int token, int i) {
+    Turn<INTER> t;
     const int half = r.rotary / 2;
-    t.on = 4 * i < half;
+    t.on = 8 * i < half;
+    t.zero = f2(r.minus_zero, r.minus_zero);
     if (r.rotary == 0) return t;
     int pos = r.positions[token];
     if (pos < 0 || pos >= r.rows) {
@@ -93,35 +102,57 @@ __device__ __forceinline__ Turn load_turn(const RotaryArgs &r, int token, int i)
         pos = 0;
     }
     if (t.on) {
-        // pairs 4 i .. 4 i + 3 in both forms
-        const int64_t at = static_cast<int64_t>(pos) * half + 4 * i;
-        const float4 c = *reinterpret_cast<const float4 *>(r.cos + at);
-        const float4 s = *reinterpret_cast<const float4 *>(r.sin + at);
-        t.c[0] = c.x, t.c[1] = c.y, t.c[2] = c.z, t.c[3] = c.w;
-        t.s[0] = s.x, t.s[1] = s.y, t.s[2] = s.z, t.s[3] = s.w;
+        // pairs 8 i .. 8 i + 7 in both forms
+        const int64_t at = static_cast<int64_t>(pos) * half + 8 * i;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float4 c = *reinterpret_cast<const float4 *>(r.cos + at + 4 * h);
+            const float4 s = *reinterpret_cast<const float4 *>(r.sin + at + 4 * h);
+            if constexpr (INTER) {
+                t.c[4 * h] = f2(c.x, c.x), t.c[4 * h + 1] = f2(c.y, c.y);
+                t.c[4 * h + 2] = f2(c.z, c.z), t.c[4 * h + 3] = f2(c.w, c.w);
+                t.s[4 * h] = f2(-s.x, s.x), t.s[4 * h + 1] = f2(-s.y, s.y);
+                t.s[4 * h + 2] = f2(-s.z, s.z), t.s[4 * h + 3] = f2(-s.w, s.w);
+            } else {
+                t.c[2 * h] = f2(c.x, c.y), t.c[2 * h + 1] = f2(c.z, c.w);
+                t.s[2 * h] = f2(-s.x, -s.y), t.s[2 * h + 1] = f2(-s.z, -s.w);
+                t.n[2 * h] = f2(s.x, s.y), t.n[2 * h + 1] = f2(s.z, s.w);
+            }
+        }
     }
     return t;
 }
 
-// Rotate a lane's channels x (pairs 0, 1: the run at a; 2, 3: the run at b) in
-// IEEE steps, each product and each sum rounded: the values, and so the codes
-// made of them, are then the same wherever they are computed.  (Paired
-// products followed by a paired sum came out with one rounding instead of two.)
-template <bool INTER>
-__device__ __forceinline__ void rotate(const Turn &t, uint64_t (&x)[4]) {
+// x c + y s.  EXACT: in IEEE steps, each product and the sum rounded: the
+// values, and so the codes made of them, are then the same wherever they are
+// computed.  (A paired product followed by a paired sum came out with one
+// rounding instead of two; as a sum with a -0 that the compiler does not know
+// the product is rounded by itself.)
+template <bool EXACT>
+__device__ __forceinline__ uint64_t turned(uint64_t x, uint64_t c, uint64_t y, uint64_t s, uint64_t zero) {
+    if (EXACT) return f2_add(f2_fma(x, c, zero), f2_fma(y, s, zero));
+    return f2_fma(x, c, f2_mul(y, s));
+}
+
+// Rotate a lane's channels x (words 0-3: the run at a; 4-7: the run at b).
+template <bool INTER, bool EXACT>
+__device__ __forceinline__ void rotate(const Turn<INTER> &t, uint64_t (&x)[8]) {
     if (!t.on) return;
-    float v[8];
+    if constexpr (INTER) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f2_split(x[i], v[2 * i], v[2 * i + 1]);
+        for (int i = 0; i < 8; ++i) {
+            float a, b;
+            f2_split(x[i], a, b);
+            x[i] = turned<EXACT>(x[i], t.c[i], f2(b, a), t.s[i], t.zero);
+        }
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : i + 4;
-        const float a = v[ia], b = v[ib];
-        v[ia] = __fsub_rn(__fmul_rn(a, t.c[i]), __fmul_rn(b, t.s[i]));
-        v[ib] = __fadd_rn(__fmul_rn(b, t.c[i]), __fmul_rn(a, t.s[i]));
+        for (int i = 0; i < 4; ++i) {
+            const uint64_t a = x[i], b = x[i + 4];
+            x[i] = turned<EXACT>(a, t.c[i], b, t.s[i], t.zero);
+            x[i + 4] = turned<EXACT>(b, t.c[i], a, t.n[i], t.zero);
+        }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = f2(v[2 * i], v[2 * i + 1]);
 }
 
 // Which token and which rows of it a warp takes: a CTA holds `wt` warps of
@@ -143,76 +174,85 @@ __device__ __forceinline__ Place place(int tokens, int wt, int tpc, int rows) {
 // ------------------------------------------------------------------ norm + rotation
 template <int D, bool INTER, int U>
 __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const QkArgs a, int wt, int tpc) {
-    constexpr int LPR = D / 8, RPW = 32 / LPR;
+    constexpr int LPR = D / 16, RPW = 32 / LPR;
     const int rows = a.q_heads + a.kv_heads;
     const Place p = place<U * RPW>(a.tokens, wt, tpc, rows);
     if (!p.ok) return;
     const int lane = threadIdx.x % 32, sub = lane / LPR;
     const Runs e = runs_of<INTER>(a.rot.rotary, lane % LPR);
-    const uint16_t *q = a.q + p.token * a.q_stride, *k = a.k + p.token * a.k_stride;
-    uint2 raw[U][2];
+    // (row r of k is k[(r - q_heads) D], so its base is moved back by the q heads)
+    const uint16_t *q = a.q + p.token * a.q_stride;
+    const uint16_t *k = a.k + p.token * a.k_stride - static_cast<int64_t>(a.q_heads) * D;
+    uint4 raw[U][2];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int r = p.row0 + u * RPW + sub;
-        raw[u][0] = raw[u][1] = make_uint2(0, 0);
+        raw[u][0] = raw[u][1] = make_uint4(0, 0, 0, 0);
         if (r < rows) {
-            const uint16_t *src = r < a.q_heads ? q + r * D : k + (r - a.q_heads) * D;
-            raw[u][0] = load8(src + e.a);
-            raw[u][1] = load8(src + e.b);
+            const uint16_t *src = (r < a.q_heads ? q : k) + r * D;
+            raw[u][0] = load16(src + e.a);
+            raw[u][1] = load16(src + e.b);
         }
     }
-    const Turn t = load_turn<INTER>(a.rot, p.token, lane % LPR);
+    const Turn<INTER> t = load_turn<INTER>(a.rot, p.token, lane % LPR);
+    uint16_t *qo = a.q_out + p.token * a.q_out_stride;
+    uint16_t *ko = a.k_out + p.token * a.k_out_stride - static_cast<int64_t>(a.q_heads) * D;
+    const uint16_t *held = nullptr;  // the weight that g holds
+    uint4 g[2] = {};
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int r = p.row0 + u * RPW + sub;
         const bool is_q = r < a.q_heads;
-        uint64_t x[4];
-        unpack4(raw[u][0], x);
-        unpack4(raw[u][1], x + 2);
+        uint64_t x[8];
+        unpack8(raw[u][0], x);
+        unpack8(raw[u][1], x + 4);
         const uint16_t *gamma = is_q ? a.q_gamma : a.k_gamma;
+        if (gamma != held) {
+            held = gamma;
+            if (gamma != nullptr) g[0] = load16(gamma + e.a), g[1] = load16(gamma + e.b);
+        }
         // the sum of squares in fp32: 64 or 128 terms, at most 2^39
-        uint64_t s2 = f2_mul(x[0], x[0]);
+        uint64_t s2 = f2_mul(x[0], x[0]), s3 = f2_mul(x[4], x[4]);
 #pragma unroll
-        for (int i = 1; i < 4; ++i) s2 = f2_fma(x[i], x[i], s2);
+        for (int i = 1; i < 4; ++i) s2 = f2_fma(x[i], x[i], s2), s3 = f2_fma(x[4 + i], x[4 + i], s3);
         float ss, s1;
-        f2_split(s2, ss, s1);
+        f2_split(f2_add(s2, s3), ss, s1);
         ss += s1;
 #pragma unroll
         for (int m = 1; m < LPR; m *= 2) ss += __shfl_xor_sync(0xffffffffu, ss, m);
         if (gamma != nullptr) {
             const float rs = rsqrtf(ss * (1.0f / D) + a.eps);
             const uint64_t r2 = f2(rs, rs);
-            uint64_t g[4];
-            unpack4(load8(gamma + e.a), g);
-            unpack4(load8(gamma + e.b), g + 2);
+            uint64_t w[8];
+            unpack8(g[0], w);
+            unpack8(g[1], w + 4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = f2_mul(f2_mul(x[i], r2), g[i]);
+            for (int i = 0; i < 8; ++i) x[i] = f2_mul(f2_mul(x[i], r2), w[i]);
         }
-        if (a.rot.rotary != 0) rotate<INTER>(t, x);
+        if (a.rot.rotary != 0) rotate<INTER, false>(t, x);
         if (r < rows) {
-            uint16_t *dst = is_q ? a.q_out + p.token * a.q_out_stride + r * D
-                                 : a.k_out + p.token * a.k_out_stride + (r - a.q_heads) * D;
-            store8(dst + e.a, pack4(x));
-            store8(dst + e.b, pack4(x + 2));
+            uint16_t *dst = (is_q ? qo : ko) + r * D;
+            store16(dst + e.a, pack8(x));
+            store16(dst + e.b, pack8(x + 4));
         }
     }
 }
 
 // ------------------------------------------------------------------ append
-// The codes of eight channels, each in the low bits of its word (INT4: code + 8,
+// The codes of sixteen channels, each in the low bits of its word (INT4: code + 8,
 // which four of add up to a word of nibbles).  The product t with the
 // reciprocal is within 127 * 2^-23 = 1.6e-5 of the quotient and the rounded
 // quotient within 0.8e-5 of it, so unless t lies within 4e-5 of a half-integer
 // both round alike; t is rounded (half to even) by adding 1.5 * 2^23, whose low
 // mantissa bits then are the code.  One channel in 12500 divides.
 template <int BITS>
-__device__ __forceinline__ void codes_of(const uint64_t (&x)[4], float s, float inv, uint32_t (&c)[8]) {
+__device__ __forceinline__ void codes_of(const uint64_t (&x)[8], float s, float inv, uint32_t (&c)[16]) {
     constexpr int top = BITS == 4 ? 7 : 127, bias = BITS == 4 ? 8 : 0;
     const float kRound = 12582912.0f + bias;
     const uint64_t i2 = f2(inv, inv), k2 = f2(kRound, kRound);
     float far = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
         const uint64_t t = f2_mul(x[i], i2), m = f2_add(t, k2), d = f2_sub(t, f2_sub(m, k2));
         float a, b;
         f2_split(m, a, b);
@@ -226,7 +266,7 @@ __device__ __forceinline__ void codes_of(const uint64_t (&x)[4], float s, float 
         // the IEEE quotient; 0 / 0 and what an infinite or NaN scale gives
         // convert to zero
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 8; ++i) {
             float a, b;
             f2_split(x[i], a, b);
             c[2 * i] = bias + max(-top, min(top, __float2int_rn(__fdiv_rn(a, s))));
@@ -235,15 +275,15 @@ __device__ __forceinline__ void codes_of(const uint64_t (&x)[4], float s, float 
     }
 }
 
-// The largest magnitude of eight channels, as bits (non-negative values order
+// The largest magnitude of sixteen channels, as bits (non-negative values order
 // alike): NaN > infinity > finite, so a row that holds one keeps it in its
 // scale.  The maximum itself ignores NaN; the sum of products with zero is NaN
 // where a channel is not finite, and the bits are compared then.
-__device__ __forceinline__ uint32_t largest(const uint64_t (&x)[4]) {
+__device__ __forceinline__ uint32_t largest(const uint64_t (&x)[8]) {
     float m = 0.0f;
     uint64_t z = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
         float a, b;
         f2_split(x[i], a, b);
         m = fmaxf(fmaxf(m, fabsf(a)), fabsf(b));
@@ -254,7 +294,7 @@ __device__ __forceinline__ uint32_t largest(const uint64_t (&x)[4]) {
     f2_split(z, z0, z1);
     if (z0 + z1 != 0.0f) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 8; ++i)
             u = max(u, max(static_cast<uint32_t>(x[i]) & 0x7fffffffu,
                            static_cast<uint32_t>(x[i] >> 32) & 0x7fffffffu));
     }
@@ -262,8 +302,8 @@ __device__ __forceinline__ uint32_t largest(const uint64_t (&x)[4]) {
 }
 
 template <int D, bool INTER, int BITS, int U>
-__global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a, int wt, int tpc) {
-    constexpr int LPR = D / 8, RPW = 32 / LPR, RB = D * BITS / 8;
+__global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a, int wt, int tpc) {
+    constexpr int LPR = D / 16, RPW = 32 / LPR, RB = D * BITS / 8;
     const int H = a.cache.heads, rows = 2 * H;
     const Place p = place<U * RPW>(a.tokens, wt, tpc, rows);
     if (!p.ok) return;
@@ -275,33 +315,35 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a, i
         return;
     }
     const Runs e = runs_of<INTER>(a.rot.rotary, lane % LPR);
-    const uint16_t *ks = a.k + p.token * a.k_stride, *vs = a.v + p.token * a.v_stride;
-    uint2 raw[U][2];
+    // (row r of v is v[(r - H) D], so its base is moved back by the k heads)
+    const uint16_t *ks = a.k + p.token * a.k_stride;
+    const uint16_t *vs = a.v + p.token * a.v_stride - static_cast<int64_t>(H) * D;
+    uint4 raw[U][2];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int r = p.row0 + u * RPW + sub;
-        raw[u][0] = raw[u][1] = make_uint2(0, 0);
+        raw[u][0] = raw[u][1] = make_uint4(0, 0, 0, 0);
         if (r < rows) {
-            const uint16_t *src = r < H ? ks + r * D : vs + (r - H) * D;
-            raw[u][0] = load8(src + e.a);
-            raw[u][1] = load8(src + e.b);
+            const uint16_t *src = (r < H ? ks : vs) + r * D;
+            raw[u][0] = load16(src + e.a);
+            raw[u][1] = load16(src + e.b);
         }
     }
     const int shift = __ffs(a.cache.page_size) - 1;  // a power of two
     const int64_t page = slot >> shift, off = slot & (a.cache.page_size - 1);
     const int64_t row0 = ((page * H) << shift) + off;  // the token's row of head 0
     uint8_t *kd = static_cast<uint8_t *>(a.cache.k) + row0 * RB, *vd = static_cast<uint8_t *>(a.cache.v) + row0 * RB;
-    Turn t;
+    Turn<INTER> t;
     t.on = false;
     if (a.rot.rotary != 0 && p.row0 < H) t = load_turn<INTER>(a.rot, p.token, lane % LPR);
-    uint64_t x[U][4];
+    uint64_t x[U][8];
     float mine = 0.0f;  // of row u where lane % U == u: its largest magnitude
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int r = p.row0 + u * RPW + sub;
-        unpack4(raw[u][0], x[u]);
-        unpack4(raw[u][1], x[u] + 2);
-        if (r < H) rotate<INTER>(t, x[u]);
+        unpack8(raw[u][0], x[u]);
+        unpack8(raw[u][1], x[u] + 4);
+        if (r < H) rotate<INTER, true>(t, x[u]);
         if (BITS == 16) continue;
         uint32_t m = largest(x[u]);
 #pragma unroll
@@ -323,8 +365,8 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a, i
         uint8_t *dst = (is_k ? kd : vd) + at_head * RB;
         if (BITS == 16) {
             if (r < rows) {
-                store8(dst + 2 * e.a, pack4(x[u]));
-                store8(dst + 2 * e.b, pack4(x[u] + 2));
+                store16(dst + 2 * e.a, pack8(x[u]));
+                store16(dst + 2 * e.b, pack8(x[u] + 4));
             }
             continue;
         }
@@ -332,18 +374,25 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a, i
         const float scale = __shfl_sync(0xffffffffu, scale_u, src);
         const float inv = __shfl_sync(0xffffffffu, inv_u, src);
         if (r >= rows) continue;
-        uint32_t c[8];
+        uint32_t c[16];
         codes_of<BITS>(x[u], scale, inv, c);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {  // the run at a, the run at b
-            const uint32_t *q = c + 4 * i;
+            const uint32_t *q = c + 8 * i;
             const int at = i ? e.b : e.a;
-            if (BITS == 8)
-                *reinterpret_cast<uint32_t *>(dst + at) =
-                    __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
-            else  // 8 more in every nibble is its top bit flipped
-                *reinterpret_cast<uint16_t *>(dst + at / 2) =
-                    static_cast<uint16_t>((q[0] + q[1] * 16 + q[2] * 256 + q[3] * 4096) ^ 0x8888u);
+            if (BITS == 8) {
+                uint32_t w[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    w[j] = __byte_perm(__byte_perm(q[4 * j], q[4 * j + 1], 0x0040),
+                                       __byte_perm(q[4 * j + 2], q[4 * j + 3], 0x0040), 0x5410);
+                *reinterpret_cast<uint2 *>(dst + at) = make_uint2(w[0], w[1]);
+            } else {  // 8 more in every nibble is its top bit flipped
+                *reinterpret_cast<uint32_t *>(dst + at / 2) =
+                    __byte_perm(q[0] + q[1] * 16 + q[2] * 256 + q[3] * 4096,
+                                q[4] + q[5] * 16 + q[6] * 256 + q[7] * 4096, 0x5410) ^
+                    0x88888888u;
+            }
         }
         if (lane % LPR == 0) (is_k ? a.cache.k_scale : a.cache.v_scale)[row0 + at_head] = scale;
     }
@@ -379,7 +428,7 @@ __global__ void __launch_bounds__(256) kv_gather_kernel(const GatherArgs a, int 
             const uint8_t *src = (is_k ? kd : vd) + at_head * RB;
             if (BITS == 16) raw[u] = *reinterpret_cast<const uint4 *>(src + 2 * e0);
             if (BITS == 8) {
-                const uint2 w = load8(src + e0);
+                const uint2 w = *reinterpret_cast<const uint2 *>(src + e0);
                 raw[u].x = w.x;
                 raw[u].y = w.y;
             }
@@ -420,8 +469,7 @@ __global__ void __launch_bounds__(256) kv_gather_kernel(const GatherArgs a, int 
             const uint64_t s2 = f2(scale[u], scale[u]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = f2_mul(f2(f[2 * i], f[2 * i + 1]), s2);
-            const uint2 lo = pack4(x), hi = pack4(x + 2);
-            out = live ? make_uint4(lo.x, lo.y, hi.x, hi.y) : make_uint4(0, 0, 0, 0);
+            out = live ? pack8(x) : make_uint4(0, 0, 0, 0);
         }
         uint16_t *o = r < H ? a.k_out + p.token * a.k_stride + r * D
                             : a.v_out + p.token * a.v_stride + (r - H) * D;
@@ -444,20 +492,20 @@ Launch plan(int tokens, int rows, int per) {
     return l;
 }
 
-// Rows in flight per lane group: four hide the memory latency of a long call
-// (each warp then has 2 KB of loads outstanding); a call with too few rows to
+// Rows in flight per lane group: several hide the memory latency of a long call
+// (a warp then has 2 to 4 KB of loads outstanding); a call with too few rows to
 // fill the SMs that way takes one row a lane group, for more warps.
-bool deep(int tokens, int rows, int rpw) {
-    return static_cast<int64_t>(tokens) * rows >= static_cast<int64_t>(sm_count()) * 16 * 4 * rpw;
+bool deep(int tokens, int rows, int per) {
+    return static_cast<int64_t>(tokens) * rows >= static_cast<int64_t>(sm_count()) * 16 * per;
 }
 
 template <int D, bool INTER>
 cudaError_t run_qk(const QkArgs &a, cudaStream_t stream) {
-    constexpr int RPW = 256 / D;
+    constexpr int RPW = 512 / D, U = 2;
     const int rows = a.q_heads + a.kv_heads;
-    if (deep(a.tokens, rows, RPW)) {
-        const Launch l = plan(a.tokens, rows, 4 * RPW);
-        qk_norm_rope_kernel<D, INTER, 4><<<l.grid, l.threads, 0, stream>>>(a, l.wt, l.tpc);
+    if (deep(a.tokens, rows, U * RPW)) {
+        const Launch l = plan(a.tokens, rows, U * RPW);
+        qk_norm_rope_kernel<D, INTER, U><<<l.grid, l.threads, 0, stream>>>(a, l.wt, l.tpc);
     } else {
         const Launch l = plan(a.tokens, rows, RPW);
         qk_norm_rope_kernel<D, INTER, 1><<<l.grid, l.threads, 0, stream>>>(a, l.wt, l.tpc);
@@ -467,11 +515,11 @@ cudaError_t run_qk(const QkArgs &a, cudaStream_t stream) {
 
 template <int D, bool INTER, int BITS>
 cudaError_t run_append(const AppendArgs &a, cudaStream_t stream) {
-    constexpr int RPW = 256 / D;
+    constexpr int RPW = 512 / D, U = 2;
     const int rows = 2 * a.cache.heads;
-    if (deep(a.tokens, rows, RPW)) {
-        const Launch l = plan(a.tokens, rows, 4 * RPW);
-        kv_append_kernel<D, INTER, BITS, 4><<<l.grid, l.threads, 0, stream>>>(a, l.wt, l.tpc);
+    if (deep(a.tokens, rows, U * RPW)) {
+        const Launch l = plan(a.tokens, rows, U * RPW);
+        kv_append_kernel<D, INTER, BITS, U><<<l.grid, l.threads, 0, stream>>>(a, l.wt, l.tpc);
     } else {
         const Launch l = plan(a.tokens, rows, RPW);
         kv_append_kernel<D, INTER, BITS, 1><<<l.grid, l.threads, 0, stream>>>(a, l.wt, l.tpc);
@@ -483,7 +531,7 @@ template <int D, int BITS>
 cudaError_t run_gather(const GatherArgs &a, cudaStream_t stream) {
     constexpr int RPW = 256 / D;
     const int rows = 2 * a.cache.heads;
-    if (deep(a.tokens, rows, RPW)) {
+    if (deep(a.tokens, rows, 4 * RPW)) {
         const Launch l = plan(a.tokens, rows, 4 * RPW);
         kv_gather_kernel<D, BITS, 4><<<l.grid, l.threads, 0, stream>>>(a, l.wt, l.tpc);
     } else {

@@ -144,6 +144,7 @@ struct RotaryArgs {
     bool interleaved = false;
     const float *cos = nullptr, *sin = nullptr;
     const int32_t *positions = nullptr;
+    float minus_zero = -0.0f;  // (a value that the kernels' compiler does not know)
 };
 
 // RMS norm of each head (gamma NULL: none) and rotation; strides in elements.
