@@ -79,12 +79,11 @@ __device__ __forceinline__ Runs runs_of(int rotary, int i) {
 }
 
 // The rotation of one token, as this lane needs it.  Half-split: cosines and
-// sines of its eight pairs, two a word; s is the run b's factor in run a, minus
-// the sine, n the run a's in run b.  Adjacent pairs: one angle a word, twice,
+// sines of its eight pairs, two a word.  Adjacent pairs: one angle a word, twice,
 // the sine with the sign of its channel.
 template <bool INTER>
 struct Turn {
-    uint64_t c[INTER ? 8 : 4], s[INTER ? 8 : 4], n[INTER ? 1 : 4];
+    uint64_t c[INTER ? 8 : 4], s[INTER ? 8 : 4];
     uint64_t zero;  // -0, -0, not known to the compiler
     bool on;        // this lane's channels are rotated
 };
@@ -115,23 +114,22 @@ __device__ __forceinline__ Turn<INTER> load_turn(const RotaryArgs &r, int token,
                 t.s[4 * h + 2] = f2(-s.z, s.z), t.s[4 * h + 3] = f2(-s.w, s.w);
             } else {
                 t.c[2 * h] = f2(c.x, c.y), t.c[2 * h + 1] = f2(c.z, c.w);
-                t.s[2 * h] = f2(-s.x, -s.y), t.s[2 * h + 1] = f2(-s.z, -s.w);
-                t.n[2 * h] = f2(s.x, s.y), t.n[2 * h + 1] = f2(s.z, s.w);
+                t.s[2 * h] = f2(s.x, s.y), t.s[2 * h + 1] = f2(s.z, s.w);
             }
         }
     }
     return t;
 }
 
-// x c + y s.  EXACT: in IEEE steps, each product and the sum rounded: the
+// x c + y s (MINUS: x c - y s).  EXACT: in IEEE steps, each product and the sum rounded: the
 // values, and so the codes made of them, are then the same wherever they are
 // computed.  (A paired product followed by a paired sum came out with one
 // rounding instead of two; as a sum with a -0 that the compiler does not know
 // the product is rounded by itself.)
-template <bool EXACT>
+template <bool EXACT, bool MINUS>
 __device__ __forceinline__ uint64_t turned(uint64_t x, uint64_t c, uint64_t y, uint64_t s, uint64_t zero) {
-    if (EXACT) return f2_add(f2_fma(x, c, zero), f2_fma(y, s, zero));
-    return f2_fma(x, c, f2_mul(y, s));
+    const uint64_t a = EXACT ? f2_fma(x, c, zero) : f2_mul(x, c), b = EXACT ? f2_fma(y, s, zero) : f2_mul(y, s);
+    return MINUS ? f2_sub(a, b) : f2_add(a, b);
 }
 
 // Rotate a lane's channels x (words 0-3: the run at a; 4-7: the run at b).
@@ -143,14 +141,14 @@ __device__ __forceinline__ void rotate(const Turn<INTER> &t, uint64_t (&x)[8]) {
         for (int i = 0; i < 8; ++i) {
             float a, b;
             f2_split(x[i], a, b);
-            x[i] = turned<EXACT>(x[i], t.c[i], f2(b, a), t.s[i], t.zero);
+            x[i] = turned<EXACT, false>(x[i], t.c[i], f2(b, a), t.s[i], t.zero);
         }
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint64_t a = x[i], b = x[i + 4];
-            x[i] = turned<EXACT>(a, t.c[i], b, t.s[i], t.zero);
-            x[i + 4] = turned<EXACT>(b, t.c[i], a, t.n[i], t.zero);
+            x[i] = turned<EXACT, true>(a, t.c[i], b, t.s[i], t.zero);
+            x[i + 4] = turned<EXACT, false>(b, t.c[i], a, t.s[i], t.zero);
         }
     }
 }
@@ -173,7 +171,7 @@ __device__ __forceinline__ Place place(int tokens, int wt, int tpc, int rows) {
 
 // ------------------------------------------------------------------ norm + rotation
 template <int D, bool INTER, int U>
-__global__ void __launch_bounds__(256) qk_norm_rope_kernel(const QkArgs a, int wt, int tpc) {
+__global__ void __launch_bounds__(256, INTER ? 3 : 4) qk_norm_rope_kernel(const QkArgs a, int wt, int tpc) {
     constexpr int LPR = D / 16, RPW = 32 / LPR;
     const int rows = a.q_heads + a.kv_heads;
     const Place p = place<U * RPW>(a.tokens, wt, tpc, rows);
@@ -302,18 +300,13 @@ __device__ __forceinline__ uint32_t largest(const uint64_t (&x)[8]) {
 }
 
 template <int D, bool INTER, int BITS, int U>
-__global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a, int wt, int tpc) {
+__global__ void __launch_bounds__(256, INTER ? 3 : 4) kv_append_kernel(const AppendArgs a, int wt, int tpc) {
     constexpr int LPR = D / 16, RPW = 32 / LPR, RB = D * BITS / 8;
     const int H = a.cache.heads, rows = 2 * H;
     const Place p = place<U * RPW>(a.tokens, wt, tpc, rows);
     if (!p.ok) return;
     const int lane = threadIdx.x % 32, sub = lane / LPR;
     const int64_t slot = a.slots[p.token];
-    const int64_t limit = static_cast<int64_t>(a.cache.pages) * a.cache.page_size;
-    if (slot < 0 || slot >= limit) {  // a padded token, or a slot outside the cache: nothing is written
-        if (slot >= limit && lane == 0) atomicAdd(&g_kv_bad_index, 1u);
-        return;
-    }
     const Runs e = runs_of<INTER>(a.rot.rotary, lane % LPR);
     // (row r of v is v[(r - H) D], so its base is moved back by the k heads)
     const uint16_t *ks = a.k + p.token * a.k_stride;
@@ -328,6 +321,12 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a, int 
             raw[u][0] = load16(src + e.a);
             raw[u][1] = load16(src + e.b);
         }
+    }
+    // (the slot is looked at only now: the rows are on their way meanwhile)
+    const int64_t limit = static_cast<int64_t>(a.cache.pages) * a.cache.page_size;
+    if (slot < 0 || slot >= limit) {  // a padded token, or a slot outside the cache: nothing is written
+        if (slot >= limit && lane == 0) atomicAdd(&g_kv_bad_index, 1u);
+        return;
     }
     const int shift = __ffs(a.cache.page_size) - 1;  // a power of two
     const int64_t page = slot >> shift, off = slot & (a.cache.page_size - 1);
