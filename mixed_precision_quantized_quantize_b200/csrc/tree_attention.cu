@@ -555,17 +555,21 @@ __global__ void __launch_bounds__(C::NW * 32) tree_attention_kernel(const Params
 // over INT4, of which 28 us remained without any arithmetic.)
 template <int BITS_, int D_>
 struct FewCfg {
-    static constexpr int BITS = BITS_, D = D_, WR = 1, NW = 4;
+    static constexpr int BITS = BITS_, D = D_, WR = 1;
     static constexpr int RB = D * BITS / 8, CPR = RB / 16;
     static constexpr int KS = RB >= 128 ? RB + 16 : RB, VS = RB + 16;
     static constexpr int SCALES = BITS == 16 ? 0 : 2 * kTile * 4;
     static constexpr int STAGE = kTile * (KS + VS) + SCALES + 32;
-    static constexpr int STAGES = STAGE > 4000 && STAGE < 6000 ? 2 : 3;
+    // warps of a CTA and stages of each: what fills an SM's shared memory with
+    // warps (one warp takes microseconds for a tile: their number counts)
+    static constexpr int NW = STAGE > 6000 ? 6 : 4;
+    static constexpr int STAGES = STAGE > 4000 ? 2 : 3;
     static constexpr int SMEM = NW * STAGES * STAGE;
     static constexpr int STEPS = D / 16, MT = D / 16;
     // resident CTAs of an SM: by 228 KB of shared memory and 65536 registers
     static constexpr int BY_SMEM = 233472 / (SMEM + 1024);
     static constexpr int CTAS = BY_SMEM < 4 ? BY_SMEM : 4;
+    static constexpr int WORKERS = CTAS * NW;  // of an SM
 };
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -1239,9 +1243,14 @@ struct Plan {
     int64_t pieces;
 };
 
+// Warps of a CTA, and of an SM.
+struct FewWarps {
+    int cta, sm;
+};
 template <int BITS>
-int few_ctas(int head_dim) {
-    return head_dim == 64 ? FewCfg<BITS, 64>::CTAS : FewCfg<BITS, 128>::CTAS;
+FewWarps few_warps(int head_dim) {
+    return head_dim == 64 ? FewWarps{FewCfg<BITS, 64>::NW, FewCfg<BITS, 64>::WORKERS}
+                          : FewWarps{FewCfg<BITS, 128>::NW, FewCfg<BITS, 128>::WORKERS};
 }
 
 // Up to eight rows: the transposed form (wr 0), with as many workers as are
@@ -1273,11 +1282,12 @@ Plan plan_of(const AttentionArgs &a) {
         return r;
     }
     if (r.wr == 0) {
-        const int ctas = a.cache.kv_type == QUIK_KV_INT4   ? few_ctas<4>(a.cache.head_dim)
-                         : a.cache.kv_type == QUIK_KV_INT8 ? few_ctas<8>(a.cache.head_dim)
-                                                           : few_ctas<16>(a.cache.head_dim);
-        const int64_t want = (items * tiles + 3) / 4, most = static_cast<int64_t>(sm_count()) * ctas;
-        r.workers = 4 * static_cast<int>(want < 1 ? 1 : want < most ? want : most);
+        const FewWarps w = a.cache.kv_type == QUIK_KV_INT4   ? few_warps<4>(a.cache.head_dim)
+                           : a.cache.kv_type == QUIK_KV_INT8 ? few_warps<8>(a.cache.head_dim)
+                                                             : few_warps<16>(a.cache.head_dim);
+        const int64_t want = items * tiles, most = static_cast<int64_t>(sm_count()) * w.sm;
+        const int64_t ctas = ((want < most ? want : most) + w.cta - 1) / w.cta;
+        r.workers = w.cta * static_cast<int>(ctas < 1 ? 1 : ctas);
         r.pieces = items + r.workers;
         return r;
     }
