@@ -25,6 +25,7 @@ using Params = AttnParams;
 constexpr int kTile = 32;          // cached tokens per tile
 constexpr float kShift = 14.0f;    // p carries 2^14
 constexpr int kMaxSplits = 64;
+constexpr int kDirectTiles = 4;    // up to 8 rows: contexts of so many tiles go to one warp whole
 // More rows of a key head than this: the tcgen05 form.  Over 4096 INT8 tokens
 // (8 sequences, 8 key heads) it takes 47-49 us whatever the rows up to 64, the
 // warp products 32 us with 16 rows, 47 with 32, 72 with 48.
@@ -603,69 +604,84 @@ __device__ __forceinline__ void enter(const Params &p, Cursor &c, int b) {
     }
 }
 
-template <class C>
+// DIRECT: a worker for each item, which writes its rows itself (short contexts,
+// where a second kernel would take as long as the first).
+template <class C, bool DIRECT>
 __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel(const Params p) {
     constexpr int BITS = C::BITS, D = C::D;
     extern __shared__ __align__(16) uint8_t smem[];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int worker = blockIdx.x * C::NW + warp;
 
-    // ---- this worker's run: the tiles of all sequences, 32 sequences at a time
-    // (the first 32 are looked at once: the usual number, and this is latency)
-    const bool report = blockIdx.x == 0 && warp == 0;
-    Seq mine{};
-    if (lane < p.sequences) mine = sequence(p, lane, report);
-    const Load mine_load = load_of(p, mine);
-    const int64_t mine_tiles = static_cast<int64_t>(mine_load.tiles) * mine_load.items;
-    int64_t all = mine_tiles;
-    for (int b = 32 + lane; b < p.sequences; b += 32) {
-        const Load l = load_of(p, sequence(p, b, report));
-        all += static_cast<int64_t>(l.tiles) * l.items;
-    }
-#pragma unroll
-    for (int x = 1; x < 32; x *= 2) all += __shfl_xor_sync(0xffffffffu, all, x);
-    // no more workers than tiles: every worker between an item's first and last has a piece of it
-    const int64_t workers = all < p.workers ? all : p.workers;
-    if (worker >= workers) return;
-    const int64_t from = all * worker / workers;
-    int left = static_cast<int>(all * (worker + 1) / workers - from);  // tiles still to be issued
+    int left;  // tiles still to be issued
     Cursor at;
     at.item = 0, at.tile = 0;
-    {
-        int64_t before = 0;
-        for (int b0 = 0; b0 < p.sequences; b0 += 32) {
-            int64_t own = mine_tiles;
-            if (b0 > 0) {
-                const Load l = load_of(p, b0 + lane < p.sequences ? sequence(p, b0 + lane, false) : Seq{});
-                own = static_cast<int64_t>(l.tiles) * l.items;
-            }
-            int64_t to = own;  // tiles up to and with this lane's sequence
+    if constexpr (DIRECT) {
+        const int per = p.heads * p.row_blocks;
+        at.b = worker / per;
+        if (at.b >= p.sequences) return;
+        at.item = worker % per;
+        at.sq = sequence(p, at.b, at.item == 0 && lane == 0);
+        const Load l = load_of(p, at.sq);
+        if (at.item >= l.items) return;
+        at.tiles = l.tiles, at.items = l.items;
+        left = l.tiles;
+    } else {
+        // ---- this worker's run: the tiles of all sequences, 32 sequences at a time
+        // (the first 32 are looked at once: the usual number, and this is latency)
+        const bool report = blockIdx.x == 0 && warp == 0;
+        Seq mine{};
+        if (lane < p.sequences) mine = sequence(p, lane, report);
+        const Load mine_load = load_of(p, mine);
+        const int64_t mine_tiles = static_cast<int64_t>(mine_load.tiles) * mine_load.items;
+        int64_t all = mine_tiles;
+        for (int b = 32 + lane; b < p.sequences; b += 32) {
+            const Load l = load_of(p, sequence(p, b, report));
+            all += static_cast<int64_t>(l.tiles) * l.items;
+        }
 #pragma unroll
-            for (int x = 1; x < 32; x *= 2) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, to, x);
-                if (lane >= x) to += y;
-            }
-            to += before;
-            const unsigned past = __ballot_sync(0xffffffffu, to > from);
-            if (past != 0) {
-                const int src = __ffs(past) - 1;
-                const int64_t ahead = from - __shfl_sync(0xffffffffu, to - own, src);
-                if (b0 == 0) {
-                    at.b = src;
-                    at.sq.first = __shfl_sync(0xffffffffu, mine.first, src);
-                    at.sq.n = __shfl_sync(0xffffffffu, mine.n, src);
-                    at.sq.ctx = __shfl_sync(0xffffffffu, mine.ctx, src);
-                    at.sq.total = __shfl_sync(0xffffffffu, mine.total, src);
-                    const Load l = load_of(p, at.sq);
-                    at.tiles = l.tiles, at.items = l.items;
-                } else {
-                    enter(p, at, b0 + src);
+        for (int x = 1; x < 32; x *= 2) all += __shfl_xor_sync(0xffffffffu, all, x);
+        // no more workers than tiles: every worker between an item's first and last has a piece of it
+        const int64_t workers = all < p.workers ? all : p.workers;
+        if (worker >= workers) return;
+        const int64_t from = all * worker / workers;
+        left = static_cast<int>(all * (worker + 1) / workers - from);
+        {
+            int64_t before = 0;
+            for (int b0 = 0; b0 < p.sequences; b0 += 32) {
+                int64_t own = mine_tiles;
+                if (b0 > 0) {
+                    const Load l = load_of(p, b0 + lane < p.sequences ? sequence(p, b0 + lane, false) : Seq{});
+                    own = static_cast<int64_t>(l.tiles) * l.items;
                 }
-                at.item = static_cast<int>(ahead / at.tiles);
-                at.tile = static_cast<int>(ahead % at.tiles);
-                break;
+                int64_t to = own;  // tiles up to and with this lane's sequence
+#pragma unroll
+                for (int x = 1; x < 32; x *= 2) {
+                    const int64_t y = __shfl_up_sync(0xffffffffu, to, x);
+                    if (lane >= x) to += y;
+                }
+                to += before;
+                const unsigned past = __ballot_sync(0xffffffffu, to > from);
+                if (past != 0) {
+                    const int src = __ffs(past) - 1;
+                    const int64_t ahead = from - __shfl_sync(0xffffffffu, to - own, src);
+                    if (b0 == 0) {
+                        at.b = src;
+                        at.sq.first = __shfl_sync(0xffffffffu, mine.first, src);
+                        at.sq.n = __shfl_sync(0xffffffffu, mine.n, src);
+                        at.sq.ctx = __shfl_sync(0xffffffffu, mine.ctx, src);
+                        at.sq.total = __shfl_sync(0xffffffffu, mine.total, src);
+                        const Load l = load_of(p, at.sq);
+                        at.tiles = l.tiles, at.items = l.items;
+                    } else {
+                        enter(p, at, b0 + src);
+                    }
+                    at.item = static_cast<int>(ahead / at.tiles);
+                    at.tile = static_cast<int>(ahead % at.tiles);
+                    break;
+                }
+                before = __shfl_sync(0xffffffffu, to, 31);
             }
-            before = __shfl_sync(0xffffffffu, to, 31);
         }
     }
     int todo = left;
@@ -681,6 +697,7 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel
     };
     locate();
     id = src.page_of(at.tile);
+    const int first_items = at.items, first_n = at.sq.n;
     // copies of the next tile, what the products need to know of it, and one step on
     bool start = true;
     auto issue = [&](int stage) {
@@ -1011,16 +1028,13 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel
                 }
             }
         }
-        if (place.w & 12) {
-            const int64_t blocks = (p.max_tokens * static_cast<int64_t>(p.group) + 7) / 8;
-            int *span = p.item_span + 2 * (place.z * (p.heads * blocks) + place.y);
-            if (lane == 0 && (place.w & 4)) span[0] = worker;
-            if (lane == 0 && (place.w & 8)) span[1] = worker;
-        }
+        if constexpr (DIRECT) continue;
+        const int64_t item = place.z * (static_cast<int64_t>(p.heads) * p.row_blocks) + place.y;
+        if (lane == 0 && (place.w & 4)) p.item_span[2 * item] = worker;
+        if (lane == 0 && (place.w & 8)) p.item_span[2 * item + 1] = worker;
         if (place.w & 2) {
             // ---- the piece, as the lanes hold it; rows that do not exist are left out
-            const int64_t blocks = (p.max_tokens * static_cast<int64_t>(p.group) + 7) / 8;
-            const int64_t item = place.z * (p.heads * blocks) + place.y, piece = worker + item;
+            const int64_t piece = worker + item;
             const float up = BITS == 16 ? 1.0f : __uint_as_float(static_cast<unsigned>(127 + R) << 23);
             float4 *dst = p.piece_o + piece * (C::MT * 32) + lane;
             if (tok[0] >= 0) {
@@ -1037,16 +1051,53 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel
             }
         }
     }
+    if constexpr (DIRECT) {
+        // ---- the rows, through shared memory into their order (the ring is done with)
+        copy_wait<0>();
+        __syncwarp();
+        static_assert(8 * (D + 4) * 4 + 32 <= C::STAGES * C::STAGE, "the rows fit the warp's ring");
+        float *rows = reinterpret_cast<float *>(ring), *lse = rows + 8 * (D + 4);
+        const float up = BITS == 16 ? 1.0f : __uint_as_float(static_cast<unsigned>(127 + R) << 23);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float sum = l[e];
+#pragma unroll
+            for (int y = 4; y < 32; y *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, y);
+            const float f = sum == 0.0f ? 0.0f : up / sum;
+            if (q8 == 0)
+                lse[2 * q4 + e] = sum == 0.0f ? -INFINITY : (m[e] - kShift + log2f(sum)) * 0.693147180559945f;
+#pragma unroll
+            for (int c = 0; c < C::MT; ++c)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    rows[(2 * q4 + e) * (D + 4) + (BITS == 16 ? 16 * c + 8 * x + q8 : q8 * (D / 8) + 2 * c + x)] =
+                        o[c][2 * x + e] * f;
+        }
+        __syncwarp();
+        const int blocks = first_items / p.heads, h = first_item / blocks, r0 = first_item % blocks * 8;
+        constexpr int PER = 8, LANES = D / PER;  // 16 bytes a lane
+#pragma unroll
+        for (int x = lane / LANES; x < 8; x += 32 / LANES) {
+            const int g = r0 + x;
+            if (g >= first_n * p.group) break;
+            const int64_t token = first + g / p.group, head = h * p.group + g % p.group;
+            const float *src8 = rows + x * (D + 4) + lane % LANES * PER;
+            const float4 a = *reinterpret_cast<const float4 *>(src8), c = *reinterpret_cast<const float4 *>(src8 + 4);
+            *reinterpret_cast<uint4 *>(p.out + token * p.out_stride + head * D + lane % LANES * PER) =
+                make_uint4(half2_of(a.x, a.y), half2_of(a.z, a.w), half2_of(c.x, c.y), half2_of(c.z, c.w));
+            if (lane % LANES == 0 && p.lse != nullptr) p.lse[token * p.q_heads + head] = lse[x];
+        }
+    }
 }
 
-// Join an item's pieces: a block of four warps a row, each warp every fourth
-// piece.  A lane's 16 bytes of a piece hold two channels of this row (and of
-// the row beside it); up to 16 pieces are loaded at once, before their maximum
-// is known.
-template <class C>
-__global__ void __launch_bounds__(128) tree_attention_few_join_kernel(const Params p) {
+// Join an item's pieces: a block of W warps a row, each warp every W-th piece.
+// A lane's 16 bytes of a piece hold two channels of this row (and of the row
+// beside it); up to 4 W pieces are loaded at once, before their maximum is
+// known.
+template <class C, int W>
+__global__ void __launch_bounds__(32 * W) tree_attention_few_join_kernel(const Params p) {
     constexpr int D = C::D, V = D / 64, AHEAD = 4;
-    __shared__ float acc_s[4][D], sum_s[4], max_s[4];
+    __shared__ float acc_s[W][D], sum_s[W], max_s[W];
     const int h = blockIdx.y, b = blockIdx.z, g = blockIdx.x;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const Seq sq = sequence(p, b, false);  // (not written by the kernel that is waited for)
@@ -1054,8 +1105,7 @@ __global__ void __launch_bounds__(128) tree_attention_few_join_kernel(const Para
     if (g >= sq.n * p.group) return;
     const Load ld = load_of(p, sq);
     const int r = g % 8, item = h * (ld.items / p.heads) + g / 8;
-    const int64_t blocks = (p.max_tokens * static_cast<int64_t>(p.group) + 7) / 8;
-    const int64_t index = b * (p.heads * blocks) + item;
+    const int64_t index = b * (static_cast<int64_t>(p.heads) * p.row_blocks) + item;
     int w0 = 0, count = 0;
     if (ld.tiles > 0) {
         const int2 span = *reinterpret_cast<const int2 *>(p.item_span + 2 * index);
@@ -1072,7 +1122,7 @@ __global__ void __launch_bounds__(128) tree_attention_few_join_kernel(const Para
     float M = -INFINITY;
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
-        const int s = warp + 4 * i;
+        const int s = warp + W * i;
         const bool ok = s < count;
         a[i] = ok ? ml[s * 8] : make_float2(-INFINITY, 0.0f);
 #pragma unroll
@@ -1080,12 +1130,13 @@ __global__ void __launch_bounds__(128) tree_attention_few_join_kernel(const Para
             v[i][j] = ok ? src[static_cast<int64_t>(s) * (C::MT * 32) + j * 128] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         M = fmaxf(M, a[i].x);
     }
-    for (int s = 4 * AHEAD + threadIdx.x; s < count; s += 128) M = fmaxf(M, ml[s * 8].x);
+    for (int s = W * AHEAD + threadIdx.x; s < count; s += 32 * W) M = fmaxf(M, ml[s * 8].x);
 #pragma unroll
     for (int y = 1; y < 32; y *= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, y));
     if (lane == 0) max_s[warp] = M;
     __syncthreads();
-    M = fmaxf(fmaxf(max_s[0], max_s[1]), fmaxf(max_s[2], max_s[3]));
+#pragma unroll
+    for (int y = 0; y < W; ++y) M = fmaxf(M, max_s[y]);
     const float base = M == -INFINITY ? 0.0f : M;
     float acc[V][2] = {}, L = 0.0f;
     auto add = [&](const float2 &m, const float4 (&x)[V]) {
@@ -1100,7 +1151,7 @@ __global__ void __launch_bounds__(128) tree_attention_few_join_kernel(const Para
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) add(a[i], v[i]);
 #pragma unroll 4
-    for (int s = 4 * AHEAD + warp; s < count; s += 4) {
+    for (int s = W * AHEAD + warp; s < count; s += W) {
         float4 x[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) x[j] = src[static_cast<int64_t>(s) * (C::MT * 32) + j * 128];
@@ -1115,17 +1166,18 @@ __global__ void __launch_bounds__(128) tree_attention_few_join_kernel(const Para
         }
     if (lane == 0) sum_s[warp] = L;
     __syncthreads();
-    L = (sum_s[0] + sum_s[1]) + (sum_s[2] + sum_s[3]);
+    L = 0.0f;
+#pragma unroll
+    for (int y = 0; y < W; ++y) L += sum_s[y];
     const int head = h * p.group + g % p.group, token = sq.first + g / p.group;
     if (threadIdx.x < D / 2) {
         const float inv = L == 0.0f ? 0.0f : 1.0f / L;
         const int e = 2 * threadIdx.x;
-        float y[2];
+        float y0 = 0.0f, y1 = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            y[i] = ((acc_s[0][e + i] + acc_s[1][e + i]) + (acc_s[2][e + i] + acc_s[3][e + i])) * inv;
+        for (int i = 0; i < W; ++i) y0 += acc_s[i][e], y1 += acc_s[i][e + 1];
         *reinterpret_cast<uint32_t *>(p.out + static_cast<int64_t>(token) * p.out_stride + head * D + e) =
-            half2_of(y[0], y[1]);
+            half2_of(y0 * inv, y1 * inv);
     }
     if (threadIdx.x == 0 && p.lse != nullptr)
         p.lse[static_cast<int64_t>(token) * p.q_heads + head] =
@@ -1240,6 +1292,7 @@ struct Plan {
     int wide;         // > 0: the tcgen05 form, with so many blocks of 128 rows a CTA
     int wr, row_blocks, splits;
     int workers;      // up to 8 rows: warps that share the tiles
+    bool direct;      // ... of whole items each
     int64_t pieces;
 };
 
@@ -1285,8 +1338,9 @@ Plan plan_of(const AttentionArgs &a) {
         const FewWarps w = a.cache.kv_type == QUIK_KV_INT4   ? few_warps<4>(a.cache.head_dim)
                            : a.cache.kv_type == QUIK_KV_INT8 ? few_warps<8>(a.cache.head_dim)
                                                              : few_warps<16>(a.cache.head_dim);
-        const int64_t want = items * tiles, most = static_cast<int64_t>(sm_count()) * w.sm;
-        const int64_t ctas = ((want < most ? want : most) + w.cta - 1) / w.cta;
+        r.direct = tiles <= kDirectTiles;
+        const int64_t want = r.direct ? items : items * tiles, most = static_cast<int64_t>(sm_count()) * w.sm;
+        const int64_t ctas = ((want < most || r.direct ? want : most) + w.cta - 1) / w.cta;
         r.workers = w.cta * static_cast<int>(ctas < 1 ? 1 : ctas);
         r.pieces = items + r.workers;
         return r;
@@ -1301,6 +1355,7 @@ Plan plan_of(const AttentionArgs &a) {
 }
 
 size_t partial_bytes(const AttentionArgs &a, const Plan &r) {
+    if (r.direct) return 0;
     if (r.wide == 0 && r.wr == 0)
         return static_cast<size_t>(r.pieces) * 8 * (a.cache.head_dim * 4 + 8) +
                static_cast<size_t>(r.pieces - r.workers) * 8;
@@ -1333,11 +1388,15 @@ quik_status join_splits(const Params &p, cudaStream_t stream) {
 
 template <class C>
 quik_status run_few(const Params &p, cudaStream_t stream) {
-    void (*kernel)(Params) = &tree_attention_few_kernel<C>;
+    void (*kernel)(Params) = p.direct ? &tree_attention_few_kernel<C, true> : &tree_attention_few_kernel<C, false>;
     if (!attribute_set_once(reinterpret_cast<const void *>(kernel), C::SMEM)) return QUIK_ERR_CUDA;
     kernel<<<p.workers / C::NW, C::NW * 32, C::SMEM, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return QUIK_ERR_CUDA;
-    return launch_join(p, &tree_attention_few_join_kernel<C>, 128, stream);
+    if (p.direct) return QUIK_OK;
+    // many pieces an item: more warps, so that a few rounds of loads see them all
+    const int64_t items = static_cast<int64_t>(p.sequences) * p.heads * p.row_blocks;
+    if (p.workers >= 48 * items) return launch_join(p, &tree_attention_few_join_kernel<C, 16>, 512, stream);
+    return launch_join(p, &tree_attention_few_join_kernel<C, 4>, 128, stream);
 }
 
 template <class C>
@@ -1402,6 +1461,7 @@ quik_status launch_tree_attention(const AttentionArgs &a, cudaStream_t stream) {
     p.part_ml = reinterpret_cast<float2 *>(
         a.partial + static_cast<size_t>(plan.splits) * a.tokens * a.q_heads * a.cache.head_dim);
     p.workers = plan.workers;
+    p.direct = plan.direct;
     p.piece_o = reinterpret_cast<float4 *>(a.partial);
     p.piece_ml = reinterpret_cast<float2 *>(a.partial + static_cast<size_t>(plan.pieces) * 8 * a.cache.head_dim);
     p.item_span = reinterpret_cast<int *>(p.piece_ml + plan.pieces * 8);
