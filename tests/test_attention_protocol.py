@@ -1,0 +1,152 @@
+"""The waits of the tcgen05 attention kernel on the CPU: its roles (loaders, the
+issuer of the products, two softmax groups) as the sequences of waits, arrivals
+and stage uses that their code makes, under random schedules.  Every schedule
+has to end, no role may use a stage that another still owns, and a wait by
+parity has to mean the phase it was written for."""
+import random
+
+import pytest
+
+
+class Barrier:
+    def __init__(self, need):
+        self.need, self.phase, self.count = need, 0, 0
+
+    def arrive(self):
+        self.count += 1
+        assert self.count <= self.need
+        if self.count == self.need:
+            self.phase, self.count = self.phase + 1, 0
+
+    def passed(self, index):
+        """Whether the wait for phase `index` goes on.  By parity it could be mistaken
+        for another only if that were two phases away."""
+        assert self.phase in (index, index + 1), (self.phase, index)
+        return self.phase > index
+
+
+def simulate(n, turns, stages, early, seed, patient=False, last_waits=True):
+    """n tiles; early: tiles that the loaders have in flight before the first handed
+    over (fp16: two, quantised: the conversion waits itself, none).  patient: the
+    loaders wait for a tile's stage before they hand the earlier one over.  last_waits:
+    a group waits for the product before the last one before it goes on to the last."""
+    rng = random.Random(seed)
+    full, empty = [Barrier(1) for _ in range(stages)], [Barrier(1) for _ in range(stages)]
+    s_full = [[Barrier(1), Barrier(1)] for _ in range(2)]
+    p_full = [[Barrier(1), Barrier(1)] for _ in range(2)]
+    pv = [Barrier(1), Barrier(1)]
+    tile_of = lambda t, g: 2 * t + g if turns else t  # noqa: E731
+    steps = lambda g: (n + 1 - g) // 2 if turns else n  # noqa: E731
+    holds = {}   # stage -> tile being read
+    queue = []   # products in order: (what to do when they are done)
+
+    def loaders():
+        for t in range(n + early):
+            if early and not patient and t >= early:
+                yield lambda: True
+                full[(t - early) % stages].arrive()
+            if t < n:
+                if t >= stages:
+                    yield lambda t=t: empty[t % stages].passed(t // stages - 1)
+                assert t % stages not in holds, "a stage is filled while it is read"
+                holds[t % stages] = t
+                if not early:
+                    full[t % stages].arrive()
+            if early and patient and t >= early:
+                full[(t - early) % stages].arrive()
+            yield lambda: True
+
+    def score(t, g):
+        tile = tile_of(t, g)
+        if turns or g == 0:
+            yield lambda: full[tile % stages].passed(tile // stages)
+
+        def done():
+            assert holds[tile % stages] == tile
+            s_full[g][t & 1].arrive()
+        queue.append(done)
+
+    def values(t, g):
+        tile = tile_of(t, g)
+        yield lambda: p_full[g][t & 1].passed(t >> 1)
+
+        def done():
+            assert holds[tile % stages] == tile
+            pv[g].arrive()
+            if turns or g == 1:
+                del holds[tile % stages]
+                empty[tile % stages].arrive()
+        queue.append(done)
+
+    def issuer():
+        for t in range(steps(0) + 1):
+            if turns:
+                for g in range(2):
+                    if t < steps(g):
+                        yield from score(t, g)
+                    if 0 < t <= steps(g):
+                        yield from values(t - 1, g)
+            else:
+                for g in range(2):
+                    if t < n:
+                        yield from score(t, g)
+                for g in range(2):
+                    if t > 0:
+                        yield from values(t - 1, g)
+
+    def softmax(g):
+        for t in range(steps(g)):
+            tile = tile_of(t, g)
+            yield lambda tile=tile: full[tile % stages].passed(tile // stages)
+            yield lambda t=t: s_full[g][t & 1].passed(t >> 1)
+            assert holds[tile % stages] == tile  # its scales and masks are still there
+            # the maximum moves: O has to stand still (and at the last tile in any case)
+            if t > 0 and (rng.random() < 0.5 or (t == steps(g) - 1 and last_waits)):
+                yield lambda t=t: pv[g].passed(t - 1)
+            p_full[g][t & 1].arrive()
+        if steps(g):
+            yield lambda: pv[g].passed(steps(g) - 1)
+
+    roles = {}
+    for name, r in (("loaders", loaders()), ("issuer", issuer()), ("softmax 0", softmax(0)), ("softmax 1", softmax(1))):
+        try:
+            roles[name] = [r, next(r)]
+        except StopIteration:
+            pass
+    while roles or queue:
+        ready = [k for k, (_, c) in roles.items() if c()]
+        moves = ready + (["product"] if queue else [])
+        if not moves:
+            return False  # nobody can go on
+        k = rng.choice(moves)
+        if k == "product":
+            queue.pop(0)()
+            continue
+        try:
+            roles[k][1] = next(roles[k][0])
+        except StopIteration:
+            del roles[k]
+    assert not holds
+    return True
+
+
+@pytest.mark.parametrize("turns", [False, True])
+@pytest.mark.parametrize("stages,early", [(4, 2), (3, 0)])  # fp16; INT8 and INT4
+@pytest.mark.parametrize("n", [0, 1, 2, 3, 4, 5, 8, 13, 24])
+def test_every_schedule_ends(turns, stages, early, n):
+    for seed in range(60):
+        assert simulate(n, turns, stages, early, seed)
+
+
+def test_a_stuck_order_is_seen():
+    """Loaders that wait for a stage before handing the tile over that would free it
+    (with the groups taking turns) get stuck, and the model says so."""
+    assert not any(simulate(24, True, 4, 2, seed, patient=True) for seed in range(20))
+
+
+def test_a_wait_for_the_wrong_phase_is_seen():
+    """Without the wait at the last tile, the last wait may meet a barrier two phases
+    behind, which its parity cannot tell from the right one."""
+    with pytest.raises(AssertionError):
+        for seed in range(60):
+            simulate(8, False, 3, 0, seed, last_waits=False)
