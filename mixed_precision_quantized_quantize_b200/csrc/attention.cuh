@@ -34,8 +34,7 @@ struct AttnParams {
 };
 
 // The tcgen05 form (tree_attention_wide.cu): `blocks` (1 or 2) blocks of 128
-// rows a CTA, p.row_blocks of those and p.splits set by the caller (one block:
-// an even number of splits, two a CTA, which are always joined).
+// rows a CTA, p.row_blocks of those and p.splits set by the caller.
 quik_status launch_attention_wide(const AttnParams &p, int kv_type, int head_dim, int blocks,
                                   cudaStream_t stream);
 

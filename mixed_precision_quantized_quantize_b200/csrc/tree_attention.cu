@@ -1327,14 +1327,11 @@ Plan plan_of(const AttentionArgs &a) {
         // one CTA an SM: the number of splits with the least time, counted in tiles
         // of 64 tokens (start and end of a CTA about four, joining about six)
         const int64_t sms = sm_count(), long_tiles = (tiles + 1) / 2;
-        // (one row block: two groups take the tiles of a CTA in turn)
         int64_t best = INT64_MAX;
-        for (int s = 1; s <= kMaxSplits / 2 && (s == 1 || long_tiles >= 4 * s); ++s) {
-            const int64_t each = ((long_tiles + s - 1) / s + (r.wide == 1 ? 1 : 0)) / (r.wide == 1 ? 2 : 1);
-            const int64_t cost = (ctas * s + sms - 1) / sms * (each + 4) + (s > 1 || r.wide == 1 ? 6 : 0);
+        for (int s = 1; s <= kMaxSplits && (s == 1 || long_tiles >= 4 * s); ++s) {
+            const int64_t cost = (ctas * s + sms - 1) / sms * ((long_tiles + s - 1) / s + 4) + (s > 1 ? 6 : 0);
             if (cost < best) best = cost, r.splits = s;
         }
-        if (r.wide == 1) r.splits *= 2;
         return r;
     }
     if (r.wr == 0) {

@@ -12,9 +12,7 @@
 // image, [64 tokens][64 channels] blocks in the 128-byte swizzle: K is read
 // along its rows (K-major), V across them (MN-major, the transpose bit of B).
 // S is double-buffered, so the products of tile t + 1 run under the softmax of
-// tile t, and the two groups' softmaxes under each other's products.  With one
-// block of rows (up to 128) both groups have it, and take the tiles in turn:
-// each is a split of its own for the join.
+// tile t, and the two row blocks' softmaxes under each other's products.
 //
 // The running maximum is only moved when a row's scores exceed it by 5 in log2
 // (p carries 2^10 here, so p <= 2^15 < 65504): rescaling O is a trip through
@@ -37,16 +35,12 @@ constexpr float kWideShift = 10.0f;  // p carries 2^10
 constexpr float kJoinShift = 14.0f;  // what the join takes p to carry
 constexpr int kLoaders = 96;     // 12 warps in all with two row blocks: 168 registers a thread
 
-// QT groups of four softmax warps.  BLOCKS row blocks: as many as groups, or one
-// (the groups then take turns).
-template <int BITS_, int D_, int BLOCKS_>
+template <int BITS_, int D_, int QT_>
 struct WideCfg {
-    static constexpr int BITS = BITS_, D = D_, QT = 2, BLOCKS = BLOCKS_;
-    static constexpr bool TURNS = BLOCKS == 1;
+    static constexpr int BITS = BITS_, D = D_, QT = QT_;
     static constexpr int RB = D * BITS / 8, CPR = RB / 16;
     static constexpr int THREADS = QT * 128 + kLoaders + 32;
-    static constexpr int OUT_BYTES = QT * 4 * 32 * 20 * 4;  // the results' way out goes through Q's place
-    static constexpr int Q_BYTES = BLOCKS * 128 * D * 2 > OUT_BYTES ? BLOCKS * 128 * D * 2 : OUT_BYTES;
+    static constexpr int Q_BYTES = QT * 128 * D * 2;
     static constexpr int HALF = kTok * D * 2;  // a K or V tile
     static constexpr int STAGES = BITS == 16 ? 4 : 3;
     static constexpr int RAW = BITS == 16 ? 0 : 2 * kTok * RB + 2 * kTok * 4;
@@ -131,26 +125,21 @@ __device__ __forceinline__ bool not_finite(uint4 w) {
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(const AttnParams p) {
     constexpr int BITS = C::BITS, D = C::D, QT = C::QT;
-    constexpr bool TURNS = C::TURNS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (ptx::smem_u32(smem_raw) & 1023)) & 1023);
     WideBars *bars = reinterpret_cast<WideBars *>(smem + C::OFF_BAR);
     // (values broadcast from lane 0 are the same in the whole warp for the compiler
     // too: the products' descriptors and loop then live in uniform registers)
     const int lane = threadIdx.x % 32, warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);
-    const int splits = TURNS ? p.splits / 2 : p.splits;  // of CTAs
-    const int split = blockIdx.x % splits, rb = blockIdx.x / splits;
+    const int split = blockIdx.x % p.splits, rb = blockIdx.x / p.splits;
     const int h = blockIdx.y, b = blockIdx.z;
     const Seq sq = sequence(p, b, blockIdx.x == 0 && h == 0 && threadIdx.x == 0);
-    const int rows = sq.n * p.group, row0 = rb * C::BLOCKS * 128;
+    const int rows = sq.n * p.group, row0 = rb * QT * 128;
     if (row0 >= rows) return;
     const int tiles = (sq.total + kTok - 1) / kTok;
-    const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * split / splits);
+    const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * split / p.splits);
     const int n = __shfl_sync(
-        0xffffffffu, static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / splits) - t0, 0);
-    // step t of group g is tile t, or 2 t + g when they take turns
-    const auto tile_of = [](int t, int g) { return TURNS ? 2 * t + g : t; };
-    const auto steps_of = [&](int g) { return TURNS ? (n + 1 - g) / 2 : n; };
+        0xffffffffu, static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / p.splits) - t0, 0);
 
     constexpr int MMA_WARP = QT * 4 + kLoaders / 32;
     if (threadIdx.x == 0) {
@@ -183,8 +172,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
         // ================================================ softmax: a thread a row
         const int g = warp / 4;
         const uint32_t lanes = static_cast<uint32_t>(warp % 4) * 32 << 16;
-        const int first_row = row0 + (TURNS ? 0 : g) * 128 + warp % 4 * 32, row = first_row + lane;
-        const int steps = steps_of(g), part = TURNS ? 2 * split + g : split;  // (of the partial results)
+        const int row = row0 + g * 128 + warp % 4 * 32 + lane;
         const int tok = row < rows ? row / p.group : -1;
         float m = -INFINITY, l = 0.0f;
         int R = -100;
@@ -194,12 +182,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
             if (tok >= 0)
                 src += static_cast<int64_t>(sq.first + tok) * p.q_stride +
                        static_cast<int64_t>(h * p.group + row % p.group) * D;
-            if (!TURNS || g == 0) {
-                const uint32_t dst = ptx::smem_u32(smem) + g * (128 * D * 2);
+            const uint32_t dst = ptx::smem_u32(smem) + g * (128 * D * 2);
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c)
-                    copy16(dst + swizzled((warp % 4) * 32 + lane, c, 128), src + 8 * c, tok >= 0);
-            }
+            for (int c = 0; c < D / 8; ++c) copy16(dst + swizzled((warp % 4) * 32 + lane, c, 128), src + 8 * c, tok >= 0);
             copy_commit();
             uint32_t z[32];
 #pragma unroll
@@ -211,11 +196,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
             ptx::mbar_arrive(&bars->q_full);
         }
         bool alive = true;
-        for (int t = 0; t < steps; ++t) {
-            const int tile = tile_of(t, g), stage = tile % C::STAGES, buf = t & 1;
+        for (int t = 0; t < n; ++t) {
+            const int stage = t % C::STAGES, buf = t & 1;
             const uint8_t *meta = smem + C::OFF_META + stage * C::META;
             // (the tile's scales and masks come from the loaders, S from the products)
-            alive = all_of(wide_wait(&bars->kv_full[stage], (tile / C::STAGES) & 1, abort) &&
+            alive = all_of(wide_wait(&bars->kv_full[stage], (t / C::STAGES) & 1, abort) &&
                            wide_wait(&bars->s_full[g][buf], (t >> 1) & 1, abort));
             if (!alive) break;
             ptx::tc_fence_after();
@@ -333,7 +318,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
                     for (int half = 0; half < 2; ++half)
 #pragma unroll 1
                         for (unsigned odd = odds[half]; odd != 0; odd &= odd - 1) {
-                            const int x = __ffs(odd) - 1, pos = (t0 + tile) * kTok + 32 * half + x;
+                            const int x = __ffs(odd) - 1, pos = (t0 + t) * kTok + 32 * half + x;
                             const bool on = (see[half] >> x) & 1u;
                             uint32_t w = 0;
 #pragma unroll
@@ -373,7 +358,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
             // The last wait below is for the last product.  By its parity it would pass
             // while the product before that one is still under way: so that one is
             // waited for here, where the last cannot have started.
-            if (t > 0 && t == steps - 1) {
+            if (t > 0 && t == n - 1) {
                 alive = all_of(wide_wait(&bars->pv_done[g], (t - 1) & 1, abort));
                 if (!alive) break;
             }
@@ -382,59 +367,58 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
             ptx::tc_fence_before();
             ptx::mbar_arrive(&bars->p_full[g][buf]);
         }
-        if (alive && steps > 0) alive = all_of(wide_wait(&bars->pv_done[g], (steps - 1) & 1, abort));
+        if (alive && n > 0) alive = all_of(wide_wait(&bars->pv_done[g], (n - 1) & 1, abort));
         if (alive) {
-            // ---- results, 16 channels at a time through shared memory (Q's place: the
-            // group's last product came after every product with Q) into whole lines
+            // ---- results, 16 channels at a time through shared memory (Q's place:
+            // every product that reads it is done) into whole lines
             ptx::tmem_st_wait();
             ptx::tc_fence_after();
             float *buf = reinterpret_cast<float *>(smem) + warp * 32 * 20;
             const float up = BITS == 16 ? 1.0f : __uint_as_float(static_cast<unsigned>(127 + R) << 23);
             const float f = p.splits > 1 ? up : l == 0.0f ? 0.0f : up / l;
+            const int first_row = row0 + g * 128 + warp % 4 * 32;
             if (row < rows) {
                 const int64_t at = static_cast<int64_t>(sq.first + row / p.group) * p.q_heads + h * p.group +
                                    row % p.group;
                 if (p.splits > 1)
-                    p.part_ml[static_cast<int64_t>(part) * p.tokens * p.q_heads + at] =
+                    p.part_ml[static_cast<int64_t>(split) * p.tokens * p.q_heads + at] =
                         make_float2(m + (kJoinShift - kWideShift), l);
                 else if (p.lse != nullptr)
                     p.lse[at] = l == 0.0f ? -INFINITY : (m - kWideShift + log2f(l)) * 0.693147180559945f;
             }
-            if (steps == 0) {
-                // no tiles: zeros, and not through Q's place, which others may still fill or read
-                if (row < rows) {
-                    const int64_t token = sq.first + row / p.group, head = h * p.group + row % p.group;
-                    float4 *po = reinterpret_cast<float4 *>(
-                        p.part_o + ((static_cast<int64_t>(part) * p.tokens + token) * p.q_heads + head) * D);
-                    uint4 *qo = reinterpret_cast<uint4 *>(p.out + token * p.out_stride + head * D);
+            if (n == 0 && row < rows) {
+                // no tiles: zeros, and not through Q's place, which is still being filled
+                const int64_t token = sq.first + row / p.group, head = h * p.group + row % p.group;
+                float4 *po = reinterpret_cast<float4 *>(
+                    p.part_o + ((static_cast<int64_t>(split) * p.tokens + token) * p.q_heads + head) * D);
+                uint4 *qo = reinterpret_cast<uint4 *>(p.out + token * p.out_stride + head * D);
 #pragma unroll 1
-                    for (int i = 0; i < D / 4; ++i) {
-                        if (p.splits > 1)
-                            po[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        else if (i < D / 8)
-                            qo[i] = make_uint4(0, 0, 0, 0);
-                    }
+                for (int i = 0; i < D / 4; ++i) {
+                    if (p.splits > 1)
+                        po[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    else if (i < D / 8)
+                        qo[i] = make_uint4(0, 0, 0, 0);
                 }
             }
             // where this lane writes: four rows of partial results, or two of the output
-            float *parts[4];
+            float *part[4];
             uint16_t *out[2];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int q = first_row + (p.splits > 1 ? i * 8 + lane / 4 : i * 16 + lane / 2);
                 const int64_t token = sq.first + q / p.group, head = h * p.group + q % p.group;
-                parts[i] = nullptr;
+                part[i] = nullptr;
                 if (i < 2) out[i] = nullptr;
-                if (q >= rows || steps == 0) continue;
+                if (q >= rows || n == 0) continue;
                 if (p.splits > 1)
-                    parts[i] = p.part_o + ((static_cast<int64_t>(part) * p.tokens + token) * p.q_heads + head) * D +
+                    part[i] = p.part_o + ((static_cast<int64_t>(split) * p.tokens + token) * p.q_heads + head) * D +
                               lane % 4 * 4;
                 else if (i < 2)
                     out[i] = p.out + token * p.out_stride + head * D + lane % 2 * 8;
             }
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
-                if (steps == 0) break;
+                if (n == 0) break;
                 uint32_t o[16];
                 ptx::tmem_ld_32x32b_x16(o_col(g) + lanes + 16 * c, o);
                 ptx::tmem_ld_wait();
@@ -447,8 +431,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
                 if (p.splits > 1) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (parts[i] != nullptr)
-                            *reinterpret_cast<float4 *>(parts[i] + 16 * c) =
+                        if (part[i] != nullptr)
+                            *reinterpret_cast<float4 *>(part[i] + 16 * c) =
                                 *reinterpret_cast<const float4 *>(buf + (i * 8 + lane / 4) * 20 + lane % 4 * 4);
                 } else {
 #pragma unroll
@@ -476,19 +460,22 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
         const int64_t head = static_cast<int64_t>(h) << p.page_shift;
         const unsigned page_rows = static_cast<unsigned>(p.heads) << p.page_shift;
         const int page_mask = (1 << p.page_shift) - 1;
-        // page numbers of a tile's four groups of 16 tokens (-1: nothing there)
-        auto pages = [&](int t, int (&id)[4]) {
+        // Page numbers of a tile's four groups of 16 tokens, as the table has them (kNone:
+        // no such tokens).  They are looked at (checked) a tile later, when the loads
+        // are long done: looked at at once they cost every tile a memory latency.
+        constexpr int kNone = INT32_MIN;
+        auto pages = [&](int t, int (&raw)[4]) {
 #pragma unroll
             for (int f = 0; f < 4; ++f) {
                 const int pos = (t0 + t) * kTok + 16 * f;
-                id[f] = -1;
-                if (t < n && pos < sq.total) {
-                    const int v = table[pos >> p.page_shift];
-                    if (static_cast<unsigned>(v) < static_cast<unsigned>(p.pages))
-                        id[f] = v;
-                    else if (lt == 0 && rb == 0)
-                        atomicAdd(&g_attn_bad_index, 1u);
-                }
+                raw[f] = t < n && pos < sq.total ? table[pos >> p.page_shift] : kNone;
+            }
+        };
+        auto checked = [&](const int (&raw)[4], int (&id)[4]) {
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                id[f] = static_cast<unsigned>(raw[f]) < static_cast<unsigned>(p.pages) ? raw[f] : -1;
+                if (id[f] < 0 && raw[f] != kNone && lt == 0 && rb == 0) atomicAdd(&g_attn_bad_index, 1u);
             }
         };
         auto id_of = [](const int (&id)[4], int f) { return f & 2 ? (f & 1 ? id[3] : id[2]) : (f & 1 ? id[1] : id[0]); };
@@ -527,8 +514,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
                 copy16(dst_of(token, 1), p.v + off, ok);
             }
         };
-        int id[4];
-        pages(0, id);
+        int raw_id[4], id[4];
+        pages(0, raw_id);
         if constexpr (BITS == 16) {
             // straight into the operand tiles, two tiles ahead of the one handed over
             constexpr int AHEAD = 2;
@@ -536,8 +523,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) live[i][0] = live[i][1] = 0;
             for (int t = 0; t < n + AHEAD; ++t) {
-                // Hand over tile t - AHEAD before waiting for tile t's stage: that stage
-                // may only come free behind products with the tile handed over.
+                // tile t - AHEAD is handed over before tile t's stage is waited for, which
+                // comes free behind products with earlier tiles
                 if (t >= AHEAD) {
                     copy_wait<AHEAD - 1>();
                     const int d = t - AHEAD;
@@ -577,9 +564,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
                         !all_of(wide_wait(&bars->kv_empty[stage], (t / C::STAGES - 1) & 1, abort)))
                         break;
                     const uint32_t at = ptx::smem_u32(smem) + C::OFF_KV + stage * 2 * C::HALF;
+                    checked(raw_id, id);
+                    pages(t + 1, raw_id);
                     copies(t, id, [&](int token, int v) { return at + v * C::HALF + swizzled(token, ch, kTok); });
                     live[AHEAD - 1][0] = live_of(id, t, 0), live[AHEAD - 1][1] = live_of(id, t, 1);
-                    pages(t + 1, id);
                 }
                 copy_commit();
             }
@@ -587,6 +575,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
             uint8_t *raws = smem + C::OFF_RAW;
             int R = -100;  // the unit of the values' scales, 2^R above every one so far (warp 0)
             auto issue = [&](int t) {
+                checked(raw_id, id);
+                pages(t + 1, raw_id);
                 if (t < n) {
                     uint8_t *raw = raws + t % C::RAWS * C::RAW;
                     const uint32_t at = ptx::smem_u32(raw);
@@ -611,7 +601,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
             for (int t = 0; t < C::RAWS - 1; ++t) {
                 issue(t);
                 live[t][0] = live_of(id, t, 0), live[t][1] = live_of(id, t, 1);
-                pages(t + 1, id);
             }
             for (int t = 0; t < n; ++t) {
                 copy_wait<C::RAWS - 2>();
@@ -676,7 +665,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
                 issue(t + C::RAWS - 1);
                 live[C::RAWS - 1][0] = live_of(id, t + C::RAWS - 1, 0);
                 live[C::RAWS - 1][1] = live_of(id, t + C::RAWS - 1, 1);
-                pages(t + C::RAWS, id);
 #pragma unroll
                 for (int i = 0; i < C::RAWS - 1; ++i) live[i][0] = live[i + 1][0], live[i][1] = live[i + 1][1];
             }
@@ -691,56 +679,44 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
         const uint64_t dq = ptx::sw128_kmajor_desc(base), dk = ptx::sw128_kmajor_desc(base + C::OFF_KV);
         const uint64_t dv = mn_desc(base + C::OFF_KV + C::HALF, kTok * 128);
         const bool leader = elect_one();
-        // S of group g's step t, and O += P V of it
-        auto score = [&](int t, int g) {
-            const int tile = tile_of(t, g), stage = tile % C::STAGES;
-            if ((TURNS || g == 0) && !all_of(wide_wait(&bars->kv_full[stage], (tile / C::STAGES) & 1, abort)))
-                return false;
-            ptx::tc_fence_after();
-            if (leader) {
-                const uint64_t q = dq + (TURNS ? 0 : g * (128 * D * 2 / 16));
-                const uint64_t k = dk + static_cast<uint32_t>(stage * (2 * C::HALF / 16));
+        auto pv = [&](int t) {  // O += P V of tile t, both row blocks
+            const int stage = t % C::STAGES, buf = t & 1;
+            const uint64_t v = dv + static_cast<uint32_t>(stage * (2 * C::HALF / 16));
 #pragma unroll
-                for (int i = 0; i < C::STEPS; ++i)
-                    ptx::mma_f16(s_col(g, t & 1), q + (i / 4 * 16384 + i % 4 * 32) / 16,
-                                 k + (i / 4 * (kTok * 128) + i % 4 * 32) / 16, id_s, i > 0);
-                ptx::mma_commit(&bars->s_full[g][t & 1]);
-            }
-            return true;
-        };
-        auto values = [&](int t, int g) {
-            const int stage = tile_of(t, g) % C::STAGES, buf = t & 1;
-            if (!all_of(wide_wait(&bars->p_full[g][buf], (t >> 1) & 1, abort))) return false;
-            ptx::tc_fence_after();
-            if (leader) {
-                const uint64_t v = dv + static_cast<uint32_t>(stage * (2 * C::HALF / 16));
+            for (int g = 0; g < QT; ++g) {
+                if (!all_of(wide_wait(&bars->p_full[g][buf], (t >> 1) & 1, abort))) return false;
+                ptx::tc_fence_after();
+                if (leader) {
 #pragma unroll
-                for (int k = 0; k < kTok / 16; ++k)
-                    mma_f16_ts(o_col(g), s_col(g, buf) + 8 * k, v + k * (2048 / 16), id_o);
-                ptx::mma_commit(&bars->pv_done[g]);
-                if (TURNS || g == QT - 1) ptx::mma_commit(&bars->kv_empty[stage]);
+                    for (int k = 0; k < kTok / 16; ++k)
+                        mma_f16_ts(o_col(g), s_col(g, buf) + 8 * k, v + k * (2048 / 16), id_o);
+                    ptx::mma_commit(&bars->pv_done[g]);
+                    if (g == QT - 1) ptx::mma_commit(&bars->kv_empty[stage]);
+                }
             }
             return true;
         };
         bool alive = n == 0 || all_of(wide_wait(&bars->q_full, 0, abort));
-        // S a step ahead of O.  Turn by turn when the groups do so: the stage of group
-        // 1's next tile is the one that group 0's last gives back.
-        for (int t = 0; t <= steps_of(0) && alive; ++t) {
-            if constexpr (TURNS) {
+        for (int t = 0; t < n && alive; ++t) {
+            const int stage = t % C::STAGES, buf = t & 1;
+            alive = all_of(wide_wait(&bars->kv_full[stage], (t / C::STAGES) & 1, abort));
+            if (!alive) break;
+            ptx::tc_fence_after();
+            if (leader) {
+                const uint64_t k = dk + static_cast<uint32_t>(stage * (2 * C::HALF / 16));
 #pragma unroll
                 for (int g = 0; g < QT; ++g) {
-                    if (alive && t < steps_of(g)) alive = score(t, g);
-                    if (alive && t > 0 && t <= steps_of(g)) alive = values(t - 1, g);
+#pragma unroll
+                    for (int i = 0; i < C::STEPS; ++i)
+                        ptx::mma_f16(s_col(g, buf), dq + (g * (128 * D * 2) + i / 4 * 16384 + i % 4 * 32) / 16,
+                                     k + (i / 4 * (kTok * 128) + i % 4 * 32) / 16, id_s, i > 0);
+                    ptx::mma_commit(&bars->s_full[g][buf]);
                 }
-            } else {
-#pragma unroll
-                for (int g = 0; g < QT; ++g)
-                    if (alive && t < n) alive = score(t, g);
-#pragma unroll
-                for (int g = 0; g < QT; ++g)
-                    if (alive && t > 0) alive = values(t - 1, g);
             }
+            if (t > 0) alive = pv(t - 1);
+            if (!alive) break;
         }
+        if (alive && n > 0) pv(n - 1);
         // whatever was issued has to end before its memory is given back
         if (leader) ptx::mma_commit(&bars->drain);
         __syncwarp();
@@ -759,8 +735,7 @@ template <class C>
 quik_status run(const AttnParams &p, cudaStream_t stream) {
     void (*kernel)(AttnParams) = &tree_attention_wide_kernel<C>;
     if (!attribute_set_once(reinterpret_cast<const void *>(kernel), C::SMEM)) return QUIK_ERR_CUDA;
-    const int splits = C::TURNS ? p.splits / 2 : p.splits;
-    kernel<<<dim3(splits * p.row_blocks, p.heads, p.sequences), C::THREADS, C::SMEM, stream>>>(p);
+    kernel<<<dim3(p.splits * p.row_blocks, p.heads, p.sequences), C::THREADS, C::SMEM, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? QUIK_OK : QUIK_ERR_CUDA;
 }
 

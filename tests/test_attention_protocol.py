@@ -25,24 +25,20 @@ class Barrier:
         return self.phase > index
 
 
-def simulate(n, turns, stages, early, seed, patient=False, last_waits=True):
+def simulate(n, stages, early, seed, last_waits=True):
     """n tiles; early: tiles that the loaders have in flight before the first handed
-    over (fp16: two, quantised: the conversion waits itself, none).  patient: the
-    loaders wait for a tile's stage before they hand the earlier one over.  last_waits:
-    a group waits for the product before the last one before it goes on to the last."""
+    over (fp16: two, quantised: the conversion waits itself, none).  last_waits: a group waits for the product before the last one before it goes on to the last."""
     rng = random.Random(seed)
     full, empty = [Barrier(1) for _ in range(stages)], [Barrier(1) for _ in range(stages)]
     s_full = [[Barrier(1), Barrier(1)] for _ in range(2)]
     p_full = [[Barrier(1), Barrier(1)] for _ in range(2)]
     pv = [Barrier(1), Barrier(1)]
-    tile_of = lambda t, g: 2 * t + g if turns else t  # noqa: E731
-    steps = lambda g: (n + 1 - g) // 2 if turns else n  # noqa: E731
     holds = {}   # stage -> tile being read
     queue = []   # products in order: (what to do when they are done)
 
     def loaders():
         for t in range(n + early):
-            if early and not patient and t >= early:
+            if early and t >= early:
                 yield lambda: True
                 full[(t - early) % stages].arrive()
             if t < n:
@@ -52,60 +48,48 @@ def simulate(n, turns, stages, early, seed, patient=False, last_waits=True):
                 holds[t % stages] = t
                 if not early:
                     full[t % stages].arrive()
-            if early and patient and t >= early:
-                full[(t - early) % stages].arrive()
             yield lambda: True
 
     def score(t, g):
-        tile = tile_of(t, g)
-        if turns or g == 0:
-            yield lambda: full[tile % stages].passed(tile // stages)
+        if g == 0:
+            yield lambda: full[t % stages].passed(t // stages)
 
         def done():
-            assert holds[tile % stages] == tile
+            assert holds[t % stages] == t
             s_full[g][t & 1].arrive()
         queue.append(done)
 
     def values(t, g):
-        tile = tile_of(t, g)
         yield lambda: p_full[g][t & 1].passed(t >> 1)
 
         def done():
-            assert holds[tile % stages] == tile
+            assert holds[t % stages] == t
             pv[g].arrive()
-            if turns or g == 1:
-                del holds[tile % stages]
-                empty[tile % stages].arrive()
+            if g == 1:
+                del holds[t % stages]
+                empty[t % stages].arrive()
         queue.append(done)
 
     def issuer():
-        for t in range(steps(0) + 1):
-            if turns:
-                for g in range(2):
-                    if t < steps(g):
-                        yield from score(t, g)
-                    if 0 < t <= steps(g):
-                        yield from values(t - 1, g)
-            else:
-                for g in range(2):
-                    if t < n:
-                        yield from score(t, g)
-                for g in range(2):
-                    if t > 0:
-                        yield from values(t - 1, g)
+        for t in range(n + 1):
+            for g in range(2):
+                if t < n:
+                    yield from score(t, g)
+            for g in range(2):
+                if t > 0:
+                    yield from values(t - 1, g)
 
     def softmax(g):
-        for t in range(steps(g)):
-            tile = tile_of(t, g)
-            yield lambda tile=tile: full[tile % stages].passed(tile // stages)
+        for t in range(n):
+            yield lambda t=t: full[t % stages].passed(t // stages)
             yield lambda t=t: s_full[g][t & 1].passed(t >> 1)
-            assert holds[tile % stages] == tile  # its scales and masks are still there
+            assert holds[t % stages] == t  # its scales and masks are still there
             # the maximum moves: O has to stand still (and at the last tile in any case)
-            if t > 0 and (rng.random() < 0.5 or (t == steps(g) - 1 and last_waits)):
+            if t > 0 and (rng.random() < 0.5 or (t == n - 1 and last_waits)):
                 yield lambda t=t: pv[g].passed(t - 1)
             p_full[g][t & 1].arrive()
-        if steps(g):
-            yield lambda: pv[g].passed(steps(g) - 1)
+        if n:
+            yield lambda: pv[g].passed(n - 1)
 
     roles = {}
     for name, r in (("loaders", loaders()), ("issuer", issuer()), ("softmax 0", softmax(0)), ("softmax 1", softmax(1))):
@@ -130,18 +114,17 @@ def simulate(n, turns, stages, early, seed, patient=False, last_waits=True):
     return True
 
 
-@pytest.mark.parametrize("turns", [False, True])
 @pytest.mark.parametrize("stages,early", [(4, 2), (3, 0)])  # fp16; INT8 and INT4
 @pytest.mark.parametrize("n", [0, 1, 2, 3, 4, 5, 8, 13, 24])
-def test_every_schedule_ends(turns, stages, early, n):
+def test_every_schedule_ends(stages, early, n):
     for seed in range(60):
-        assert simulate(n, turns, stages, early, seed)
+        assert simulate(n, stages, early, seed)
 
 
 def test_a_stuck_order_is_seen():
-    """Loaders that wait for a stage before handing the tile over that would free it
-    (with the groups taking turns) get stuck, and the model says so."""
-    assert not any(simulate(24, True, 4, 2, seed, patient=True) for seed in range(20))
+    """Two tiles in flight before the first is handed over, in one stage: stuck, and
+    the model says so."""
+    assert not any(simulate(24, 1, 2, seed) for seed in range(20))
 
 
 def test_a_wait_for_the_wrong_phase_is_seen():
@@ -149,4 +132,4 @@ def test_a_wait_for_the_wrong_phase_is_seen():
     behind, which its parity cannot tell from the right one."""
     with pytest.raises(AssertionError):
         for seed in range(60):
-            simulate(8, False, 3, 0, seed, last_waits=False)
+            simulate(8, 3, 0, seed, last_waits=False)
