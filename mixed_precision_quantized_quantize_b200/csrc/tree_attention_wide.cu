@@ -20,6 +20,8 @@
 //
 // Bound by the exponentials: 256 rows x 64 tokens take the 4 x 4 lanes of an
 // SM's special-function units 1024 cycles, the products as many.
+#include <type_traits>
+
 #include "attention.cuh"
 
 namespace quik {
@@ -274,29 +276,35 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
             const uint64_t b2 = ptx::f2(base, base);
             uint64_t sum = 0;
             uint32_t pk[32];
+            auto weights = [&](auto some) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float x[4];
-                ptx::f2_split(ptx::f2_sub(ptx::f2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), b2), x[0],
-                              x[1]);
-                ptx::f2_split(ptx::f2_sub(ptx::f2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), b2),
-                              x[2], x[3]);
+                for (int i = 0; i < 16; ++i) {
+                    float x[4];
+                    ptx::f2_split(ptx::f2_sub(ptx::f2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), b2), x[0],
+                                  x[1]);
+                    ptx::f2_split(ptx::f2_sub(ptx::f2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), b2),
+                                  x[2], x[3]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] = exp2_fast(x[j]);
-                sum = ptx::f2_add(sum, ptx::f2_add(ptx::f2(x[0], x[1]), ptx::f2(x[2], x[3])));
-                if constexpr (BITS != 16) {
-                    const float4 v4 = *reinterpret_cast<const float4 *>(meta + kTok * 4 + 16 * i);
-                    ptx::f2_split(ptx::f2_mul(ptx::f2(x[0], x[1]), ptx::f2(v4.x, v4.y)), x[0], x[1]);
-                    ptx::f2_split(ptx::f2_mul(ptx::f2(x[2], x[3]), ptx::f2(v4.z, v4.w)), x[2], x[3]);
-                    if (masked) {  // an unseen token's scale may be anything
+                    for (int j = 0; j < 4; ++j) x[j] = exp2_fast(x[j]);
+                    sum = ptx::f2_add(sum, ptx::f2_add(ptx::f2(x[0], x[1]), ptx::f2(x[2], x[3])));
+                    if constexpr (BITS != 16) {
+                        const float4 v4 = *reinterpret_cast<const float4 *>(meta + kTok * 4 + 16 * i);
+                        ptx::f2_split(ptx::f2_mul(ptx::f2(x[0], x[1]), ptx::f2(v4.x, v4.y)), x[0], x[1]);
+                        ptx::f2_split(ptx::f2_mul(ptx::f2(x[2], x[3]), ptx::f2(v4.z, v4.w)), x[2], x[3]);
+                        if constexpr (decltype(some)::value) {  // an unseen token's scale may be anything
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (!((see[i / 8] >> (4 * i % 32 + j)) & 1u)) x[j] = 0.0f;
+                            for (int j = 0; j < 4; ++j)
+                                if (!((see[i / 8] >> (4 * i % 32 + j)) & 1u)) x[j] = 0.0f;
+                        }
                     }
+                    pk[2 * i] = half2_of(x[0], x[1]);
+                    pk[2 * i + 1] = half2_of(x[2], x[3]);
                 }
-                pk[2 * i] = half2_of(x[0], x[1]);
-                pk[2 * i + 1] = half2_of(x[2], x[3]);
-            }
+            };
+            if (BITS != 16 && masked)
+                weights(std::true_type{});
+            else
+                weights(std::false_type{});
             float a, c;
             ptx::f2_split(sum, a, c);
             l += a + c;
