@@ -35,19 +35,19 @@ constexpr int kTok = 64;            // cached tokens per tile
 constexpr float kLazy = 5.0f;        // how far scores may pass the running maximum (log2)
 constexpr float kWideShift = 10.0f;  // p carries 2^10
 constexpr float kJoinShift = 14.0f;  // what the join takes p to carry
-constexpr int kLoaders = 96;     // 12 warps in all with two row blocks: 168 registers a thread
+constexpr int kLoaders = 192;        // and a warp for the scales
 
 template <int BITS_, int D_, int QT_>
 struct WideCfg {
     static constexpr int BITS = BITS_, D = D_, QT = QT_;
     static constexpr int RB = D * BITS / 8, CPR = RB / 16;
-    static constexpr int THREADS = QT * 128 + kLoaders + 32;
+    static constexpr int THREADS = QT * 128 + kLoaders + 64;
     static constexpr int Q_BYTES = QT * 128 * D * 2;
     static constexpr int HALF = kTok * D * 2;  // a K or V tile
     static constexpr int STAGES = BITS == 16 ? 4 : 3;
     static constexpr int RAW = BITS == 16 ? 0 : 2 * kTok * RB + 2 * kTok * 4;
     static constexpr int RAWS = BITS == 16 ? 0 : BITS == 8 ? 3 : 4;
-    static constexpr int META = 2 * kTok * 4 + 64;  // K scales, V scales, int4, an int2 of each loader warp
+    static constexpr int META = 2 * kTok * 4 + 16 + kLoaders / 32 * 8;  // K scales, V scales, int4, an int2 a loader warp
     static constexpr int OFF_KV = Q_BYTES;
     static constexpr int OFF_RAW = OFF_KV + STAGES * 2 * HALF;
     static constexpr int OFF_META = OFF_RAW + RAWS * RAW;
@@ -66,10 +66,11 @@ struct WideBars {
 
 // Wait for a phase, for at most kWaitLimitNs and not once another role has given
 // up.  Every lane of a warp waits for itself; a warp goes by all_of its answers.
-__device__ __noinline__ bool wide_wait_slowly(uint64_t *bar, uint32_t parity, volatile int *abort) {
+__device__ __forceinline__ bool wide_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = ptx::global_timer_ns();
-    while (true) {
-        if (ptx::mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+    while (!ptx::mbar_try_wait(bar, parity)) {
         if (*abort) return false;
         if (ptx::global_timer_ns() - t0 > kWaitLimitNs) {
             *abort = 1;
@@ -77,11 +78,7 @@ __device__ __noinline__ bool wide_wait_slowly(uint64_t *bar, uint32_t parity, vo
             return false;
         }
     }
-}
-__device__ __forceinline__ bool wide_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    for (int i = 0; i < 4; ++i)
-        if (ptx::mbar_try_wait(bar, parity)) return true;
-    return wide_wait_slowly(bar, parity, abort);
+    return true;
 }
 __device__ __forceinline__ bool all_of(bool ok) { return __all_sync(0xffffffffu, ok); }
 
@@ -143,10 +140,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
     const int n = __shfl_sync(
         0xffffffffu, static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / p.splits) - t0, 0);
 
-    constexpr int MMA_WARP = QT * 4 + kLoaders / 32;
+    constexpr int MMA_WARP = QT * 4 + kLoaders / 32 + 1;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
-            ptx::mbar_init(&bars->kv_full[i], kLoaders);
+            ptx::mbar_init(&bars->kv_full[i], BITS == 16 ? kLoaders : kLoaders + 32);
             ptx::mbar_init(&bars->kv_empty[i], 1);
         }
         for (int g = 0; g < QT; ++g) {
@@ -172,6 +169,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
 
     if (warp < QT * 4) {
         // ================================================ softmax: a thread a row
+        if constexpr (QT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         const int g = warp / 4;
         const uint32_t lanes = static_cast<uint32_t>(warp % 4) * 32 << 16;
         const int row = row0 + g * 128 + warp % 4 * 32 + lane;
@@ -314,7 +312,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
                 // rows that see the token add them here
                 const uint4 w0 = *reinterpret_cast<const uint4 *>(meta + 2 * kTok * 4 + 16);
                 const uint4 w1 = *reinterpret_cast<const uint4 *>(meta + 2 * kTok * 4 + 32);
-                const unsigned odds[2] = {w0.x | w0.z | w1.x, w0.y | w0.w | w1.y};  // of three warps
+                const uint4 w2 = *reinterpret_cast<const uint4 *>(meta + 2 * kTok * 4 + 48);
+                const unsigned odds[2] = {w0.x | w0.z | w1.x | w1.z | w2.x | w2.z, w0.y | w0.w | w1.y | w1.w | w2.y | w2.w};
                 if ((odds[0] | odds[1]) != 0) {
                     if (t > 0) {
                         alive = all_of(wide_wait(&bars->pv_done[g], (t - 1) & 1, abort));
@@ -457,6 +456,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
             }
         }
     } else if (warp < MMA_WARP) {
+        if constexpr (QT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         // ================================================ loaders
         const int lt = threadIdx.x - QT * 128;
         // a thread's chunks of K (and V): the same place in rows TSTEP apart
@@ -524,7 +524,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
         };
         int raw_id[4], id[4];
         pages(0, raw_id);
-        if constexpr (BITS == 16) {
+        if (lt >= kLoaders && BITS == 16) {
+            // (no scales)
+        } else if constexpr (BITS == 16) {
             // straight into the operand tiles, two tiles ahead of the one handed over
             constexpr int AHEAD = 2;
             unsigned live[AHEAD][2];  // of tiles t - AHEAD .. t - 1
@@ -580,19 +582,25 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
                 copy_commit();
             }
         } else {
+            // a ring of tiles as they come: RAWS - 1 on their way
             uint8_t *raws = smem + C::OFF_RAW;
-            int R = -100;  // the unit of the values' scales, 2^R above every one so far (warp 0)
+            // Eight lanes write eight 16-byte chunks at a time, the lanes of the second
+            // half of a row's chunks (the second 64 channels, at the same place in their
+            // own block) in the other order: no two then meet in a bank.
+            const int turn = D == 128 ? ch / (C::CPR / 2) : 0;
+            const bool scales = lt >= kLoaders;
+            int R = -100;  // the unit of the values' scales, 2^R above every one so far
             auto issue = [&](int t) {
                 checked(raw_id, id);
                 pages(t + 1, raw_id);
                 if (t < n) {
-                    uint8_t *raw = raws + t % C::RAWS * C::RAW;
-                    const uint32_t at = ptx::smem_u32(raw);
-                    copies(t, id, [&](int token, int v) { return at + (v * kTok + token) * C::RB + ch * 16; });
-                    if (lt < 32) {
+                    const uint32_t at = ptx::smem_u32(raws + t % C::RAWS * C::RAW);
+                    if (!scales) {
+                        copies(t, id, [&](int token, int v) { return at + (v * kTok + token) * C::RB + ch * 16; });
+                    } else {
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
-                            const int token = lt + 32 * half, pid = id_of(id, token / 16);
+                            const int token = lane + 32 * half, pid = id_of(id, token / 16);
                             const bool ok = pid >= 0 && (t0 + t) * kTok + token < sq.total;
                             const int64_t r = ok ? row_of(pid, t, token) : 0;
                             copy4(at + 2 * kTok * C::RB + 4 * token, p.ks + r, ok);
@@ -616,20 +624,26 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
                 if (t >= C::STAGES && !all_of(wide_wait(&bars->kv_empty[stage], (t / C::STAGES - 1) & 1, abort))) break;
                 const uint8_t *raw = raws + t % C::RAWS * C::RAW;
                 uint8_t *kv = smem + C::OFF_KV + stage * 2 * C::HALF;
-                uint8_t *meta = smem + C::OFF_META + stage * C::META;
-                if (lt < 32) {
+                if (scales) {
                     const float *sc = reinterpret_cast<const float *>(raw + 2 * kTok * C::RB);
-                    float *ks = reinterpret_cast<float *>(meta), *vs = ks + kTok;
-                    const float v0 = sc[kTok + lt], v1 = sc[kTok + 32 + lt];
+                    float *ks = reinterpret_cast<float *>(smem + C::OFF_META + stage * C::META), *vs = ks + kTok;
+                    const float v0 = sc[kTok + lane], v1 = sc[kTok + 32 + lane];
                     const int e = top_exponent(__reduce_max_sync(0xffffffffu, max(finite_bits(v0), finite_bits(v1))));
                     if (e > R) R = min(e + 1, 126);  // some room, so that it moves less often
                     const float unit = __uint_as_float(static_cast<unsigned>(127 - R) << 23);
-                    ks[lt] = sc[lt] * p.scale_log2, ks[32 + lt] = sc[32 + lt] * p.scale_log2;
-                    vs[lt] = v0 * unit, vs[32 + lt] = v1 * unit;
-                    if (lt == 0)
-                        *reinterpret_cast<int4 *>(meta + 2 * kTok * 4) =
+                    ks[lane] = sc[lane] * p.scale_log2, ks[32 + lane] = sc[32 + lane] * p.scale_log2;
+                    vs[lane] = v0 * unit, vs[32 + lane] = v1 * unit;
+                    if (lane == 0)
+                        *reinterpret_cast<int4 *>(ks + 2 * kTok) =
                             make_int4(static_cast<int>(live[0][0]), static_cast<int>(live[0][1]),
                                       (t0 + t) * kTok - sq.ctx, R);
+                    ptx::mbar_arrive(&bars->kv_full[stage]);
+                    issue(t + C::RAWS - 1);
+                    live[C::RAWS - 1][0] = live_of(id, t + C::RAWS - 1, 0);
+                    live[C::RAWS - 1][1] = live_of(id, t + C::RAWS - 1, 1);
+#pragma unroll
+                    for (int i = 0; i < C::RAWS - 1; ++i) live[i][0] = live[i + 1][0], live[i][1] = live[i + 1][1];
+                    continue;
                 }
                 // this thread's own chunks, from codes to fp16: K's, then V's (loads first,
                 // which the compiler cannot move over the stores)
@@ -649,18 +663,19 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
                         if constexpr (BITS == 8) {
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
-                                const uint32_t a = w[2 * i] ^ 0x80808080u, c = w[2 * i + 1] ^ 0x80808080u;
-                                *reinterpret_cast<uint4 *>(dst + swizzled(token, 2 * ch + i, kTok)) =
+                                const uint32_t a = (turn ? w[2 - 2 * i] : w[2 * i]) ^ 0x80808080u;
+                                const uint32_t c = (turn ? w[3 - 2 * i] : w[2 * i + 1]) ^ 0x80808080u;
+                                *reinterpret_cast<uint4 *>(dst + swizzled(token, 2 * ch + (i ^ turn), kTok)) =
                                     make_uint4(pair8(a, false), pair8(a, true), pair8(c, false), pair8(c, true));
                             }
                         } else {
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 // pairs (0, 4), (1, 5), (2, 6), (3, 7) into channel order
-                                const uint32_t y = w[i] >> 8;
-                                const uint32_t a = pair4(w[i], false), c = pair4(w[i], true), d = pair4(y, false),
+                                const uint32_t x = turn ? w[i ^ 1] : w[i], y = x >> 8;
+                                const uint32_t a = pair4(x, false), c = pair4(x, true), d = pair4(y, false),
                                                f = pair4(y, true);
-                                *reinterpret_cast<uint4 *>(dst + swizzled(token, 4 * ch + i, kTok)) =
+                                *reinterpret_cast<uint4 *>(dst + swizzled(token, 4 * ch + (i ^ turn), kTok)) =
                                     make_uint4(pick(a, c, 0x5410u), pick(d, f, 0x5410u), pick(a, c, 0x7632u),
                                                pick(d, f, 0x7632u));
                             }
@@ -671,15 +686,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
                 ptx::mbar_arrive(&bars->kv_full[stage]);
                 // the raw slot of the tile before this one is free: refill it
                 issue(t + C::RAWS - 1);
-                live[C::RAWS - 1][0] = live_of(id, t + C::RAWS - 1, 0);
-                live[C::RAWS - 1][1] = live_of(id, t + C::RAWS - 1, 1);
-#pragma unroll
-                for (int i = 0; i < C::RAWS - 1; ++i) live[i][0] = live[i + 1][0], live[i][1] = live[i + 1][1];
             }
         }
         copy_wait<0>();
     } else {
         // ================================================ products
+        if constexpr (QT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         // (descriptors are sums of a base and constants: in the low word, whose
         // address field does not overflow below 256 KB)
         const uint32_t base = ptx::smem_u32(smem);
