@@ -672,10 +672,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 // pairs (0, 4), (1, 5), (2, 6), (3, 7) into channel order
-                                const uint32_t x = turn ? w[i ^ 1] : w[i], y = x >> 8;
+                                const uint32_t x = turn ? w[i ^ 2] : w[i], y = x >> 8;
                                 const uint32_t a = pair4(x, false), c = pair4(x, true), d = pair4(y, false),
                                                f = pair4(y, true);
-                                *reinterpret_cast<uint4 *>(dst + swizzled(token, 4 * ch + (i ^ turn), kTok)) =
+                                *reinterpret_cast<uint4 *>(dst + swizzled(token, 4 * ch + (i ^ (2 * turn)), kTok)) =
                                     make_uint4(pick(a, c, 0x5410u), pick(d, f, 0x5410u), pick(a, c, 0x7632u),
                                                pick(d, f, 0x7632u));
                             }
