@@ -174,17 +174,22 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
         const uint32_t lanes = static_cast<uint32_t>(warp % 4) * 32 << 16;
         const int row = row0 + g * 128 + warp % 4 * 32 + lane;
         const int tok = row < rows ? row / p.group : -1;
+        const int head = h * p.group + row - row / p.group * p.group;  // (of a row that is there)
         float m = -INFINITY, l = 0.0f;
         int R = -100;
         {
-            // this row of Q (zeros past the last)
-            const uint16_t *src = p.q;
-            if (tok >= 0)
-                src += static_cast<int64_t>(sq.first + tok) * p.q_stride +
-                       static_cast<int64_t>(h * p.group + row % p.group) * D;
+            // this warp's rows of Q (zeros past the last), a row's chunks by lanes beside
+            // each other; where a row starts comes from its own lane
+            constexpr int CH = D / 8;
+            const int64_t start =
+                tok < 0 ? -1 : static_cast<int64_t>(sq.first + tok) * p.q_stride + static_cast<int64_t>(head) * D;
             const uint32_t dst = ptx::smem_u32(smem) + g * (128 * D * 2);
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) copy16(dst + swizzled((warp % 4) * 32 + lane, c, 128), src + 8 * c, tok >= 0);
+            for (int i = 0; i < CH; ++i) {
+                const int r = i * (32 / CH) + lane / CH, c = lane % CH;
+                const int64_t from = __shfl_sync(0xffffffffu, start, r);
+                copy16(dst + swizzled(warp % 4 * 32 + r, c, 128), from < 0 ? p.q : p.q + from + 8 * c, from >= 0);
+            }
             copy_commit();
             uint32_t z[32];
 #pragma unroll
@@ -383,22 +388,21 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
             float *buf = reinterpret_cast<float *>(smem) + warp * 32 * 20;
             const float up = BITS == 16 ? 1.0f : __uint_as_float(static_cast<unsigned>(127 + R) << 23);
             const float f = p.splits > 1 ? up : l == 0.0f ? 0.0f : up / l;
-            const int first_row = row0 + g * 128 + warp % 4 * 32;
-            if (row < rows) {
-                const int64_t at = static_cast<int64_t>(sq.first + row / p.group) * p.q_heads + h * p.group +
-                                   row % p.group;
+            const int64_t at = tok < 0 ? -1 : static_cast<int64_t>(sq.first + tok) * p.q_heads + head;
+            const int64_t out_at =
+                tok < 0 ? -1 : (sq.first + tok) * p.out_stride + static_cast<int64_t>(head) * D;
+            if (tok >= 0) {
                 if (p.splits > 1)
                     p.part_ml[static_cast<int64_t>(split) * p.tokens * p.q_heads + at] =
                         make_float2(m + (kJoinShift - kWideShift), l);
                 else if (p.lse != nullptr)
                     p.lse[at] = l == 0.0f ? -INFINITY : (m - kWideShift + log2f(l)) * 0.693147180559945f;
             }
-            if (n == 0 && row < rows) {
+            float *const part_o = p.part_o + static_cast<int64_t>(split) * p.tokens * p.q_heads * D;
+            if (n == 0 && tok >= 0) {
                 // no tiles: zeros, and not through Q's place, which is still being filled
-                const int64_t token = sq.first + row / p.group, head = h * p.group + row % p.group;
-                float4 *po = reinterpret_cast<float4 *>(
-                    p.part_o + ((static_cast<int64_t>(split) * p.tokens + token) * p.q_heads + head) * D);
-                uint4 *qo = reinterpret_cast<uint4 *>(p.out + token * p.out_stride + head * D);
+                float4 *po = reinterpret_cast<float4 *>(part_o + at * D);
+                uint4 *qo = reinterpret_cast<uint4 *>(p.out + out_at);
 #pragma unroll 1
                 for (int i = 0; i < D / 4; ++i) {
                     if (p.splits > 1)
@@ -412,16 +416,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
             uint16_t *out[2];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int q = first_row + (p.splits > 1 ? i * 8 + lane / 4 : i * 16 + lane / 2);
-                const int64_t token = sq.first + q / p.group, head = h * p.group + q % p.group;
-                part[i] = nullptr;
-                if (i < 2) out[i] = nullptr;
-                if (q >= rows || n == 0) continue;
-                if (p.splits > 1)
-                    part[i] = p.part_o + ((static_cast<int64_t>(split) * p.tokens + token) * p.q_heads + head) * D +
-                              lane % 4 * 4;
-                else if (i < 2)
-                    out[i] = p.out + token * p.out_stride + head * D + lane % 2 * 8;
+                const int64_t y = __shfl_sync(0xffffffffu, at, i * 8 + lane / 4);
+                part[i] = y < 0 || n == 0 || p.splits == 1 ? nullptr : part_o + y * D + lane % 4 * 4;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int64_t y = __shfl_sync(0xffffffffu, out_at, i * 16 + lane / 2);
+                out[i] = y < 0 || n == 0 ? nullptr : p.out + y + lane % 2 * 8;
             }
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
