@@ -31,6 +31,7 @@ static __device__ unsigned int g_wide_waits;
 
 namespace {
 
+constexpr int kPitch = 36;          // floats of a row in the write-out's shared memory (32 of them)
 constexpr int kTok = 64;            // cached tokens per tile
 constexpr float kLazy = 5.0f;        // how far scores may pass the running maximum (log2)
 constexpr float kWideShift = 10.0f;  // p carries 2^10
@@ -48,7 +49,8 @@ struct WideCfg {
     static constexpr int RAW = BITS == 16 ? 0 : 2 * kTok * RB + 2 * kTok * 4;
     static constexpr int RAWS = BITS == 16 ? 0 : BITS == 8 ? 3 : 4;
     static constexpr int META = 2 * kTok * 4 + 16 + kLoaders / 32 * 8;  // K scales, V scales, int4, an int2 a loader warp
-    static constexpr int OFF_KV = Q_BYTES;
+    static constexpr int OUT_BYTES = QT * 128 * kPitch * 4;  // the write-out's, in Q's place
+    static constexpr int OFF_KV = Q_BYTES > OUT_BYTES ? Q_BYTES : OUT_BYTES;
     static constexpr int OFF_RAW = OFF_KV + STAGES * 2 * HALF;
     static constexpr int OFF_META = OFF_RAW + RAWS * RAW;
     static constexpr int OFF_BAR = OFF_META + STAGES * META;
@@ -169,7 +171,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
 
     if (warp < QT * 4) {
         // ================================================ softmax: a thread a row
-        if constexpr (QT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        if constexpr (QT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         const int g = warp / 4;
         const uint32_t lanes = static_cast<uint32_t>(warp % 4) * 32 << 16;
         const int row = row0 + g * 128 + warp % 4 * 32 + lane;
@@ -381,11 +383,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
         }
         if (alive && n > 0) alive = all_of(wide_wait(&bars->pv_done[g], (n - 1) & 1, abort));
         if (alive) {
-            // ---- results, 16 channels at a time through shared memory (Q's place:
+            // ---- results, 32 channels at a time through shared memory (Q's place:
             // every product that reads it is done) into whole lines
             ptx::tmem_st_wait();
             ptx::tc_fence_after();
-            float *buf = reinterpret_cast<float *>(smem) + warp * 32 * 20;
+            float *buf = reinterpret_cast<float *>(smem) + warp * 32 * kPitch;
             const float up = BITS == 16 ? 1.0f : __uint_as_float(static_cast<unsigned>(127 + R) << 23);
             const float f = p.splits > 1 ? up : l == 0.0f ? 0.0f : up / l;
             const int64_t at = tok < 0 ? -1 : static_cast<int64_t>(sq.first + tok) * p.q_heads + head;
@@ -411,45 +413,45 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
                         qo[i] = make_uint4(0, 0, 0, 0);
                 }
             }
-            // where this lane writes: four rows of partial results, or two of the output
-            float *part[4];
-            uint16_t *out[2];
+            // where this lane writes: eight rows of partial results, or four of the output
+            float *part[8];
+            uint16_t *out[4];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int64_t y = __shfl_sync(0xffffffffu, at, i * 4 + lane / 8);
+                part[i] = y < 0 || n == 0 || p.splits == 1 ? nullptr : part_o + y * D + lane % 8 * 4;
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int64_t y = __shfl_sync(0xffffffffu, at, i * 8 + lane / 4);
-                part[i] = y < 0 || n == 0 || p.splits == 1 ? nullptr : part_o + y * D + lane % 4 * 4;
+                const int64_t y = __shfl_sync(0xffffffffu, out_at, i * 8 + lane / 4);
+                out[i] = y < 0 || n == 0 ? nullptr : p.out + y + lane % 4 * 8;
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int64_t y = __shfl_sync(0xffffffffu, out_at, i * 16 + lane / 2);
-                out[i] = y < 0 || n == 0 ? nullptr : p.out + y + lane % 2 * 8;
-            }
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
+            for (int c = 0; c < D / 32; ++c) {
                 if (n == 0) break;
-                uint32_t o[16];
-                ptx::tmem_ld_32x32b_x16(o_col(g) + lanes + 16 * c, o);
+                uint32_t o[32];
+                ptx::tmem_ld_32x32b_x32(o_col(g) + lanes + 32 * c, o);
                 ptx::tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<float4 *>(buf + lane * 20 + 4 * i) =
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<float4 *>(buf + lane * kPitch + 4 * i) =
                         make_float4(__uint_as_float(o[4 * i]) * f, __uint_as_float(o[4 * i + 1]) * f,
                                     __uint_as_float(o[4 * i + 2]) * f, __uint_as_float(o[4 * i + 3]) * f);
                 __syncwarp();
                 if (p.splits > 1) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < 8; ++i)
                         if (part[i] != nullptr)
-                            *reinterpret_cast<float4 *>(part[i] + 16 * c) =
-                                *reinterpret_cast<const float4 *>(buf + (i * 8 + lane / 4) * 20 + lane % 4 * 4);
+                            *reinterpret_cast<float4 *>(part[i] + 32 * c) =
+                                *reinterpret_cast<const float4 *>(buf + (i * 4 + lane / 8) * kPitch + lane % 8 * 4);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
+                    for (int i = 0; i < 4; ++i) {
                         if (out[i] == nullptr) continue;
-                        const float *r = buf + (i * 16 + lane / 2) * 20 + lane % 2 * 8;
+                        const float *r = buf + (i * 8 + lane / 4) * kPitch + lane % 4 * 8;
                         const float4 x = *reinterpret_cast<const float4 *>(r);
                         const float4 y = *reinterpret_cast<const float4 *>(r + 4);
-                        *reinterpret_cast<uint4 *>(out[i] + 16 * c) =
+                        *reinterpret_cast<uint4 *>(out[i] + 32 * c) =
                             make_uint4(half2_of(x.x, x.y), half2_of(x.z, x.w), half2_of(y.x, y.y), half2_of(y.z, y.w));
                     }
                 }
@@ -457,7 +459,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
             }
         }
     } else if (warp < MMA_WARP) {
-        if constexpr (QT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if constexpr (QT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         // ================================================ loaders
         const int lt = threadIdx.x - QT * 128;
         // a thread's chunks of K (and V): the same place in rows TSTEP apart
@@ -692,7 +694,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
         copy_wait<0>();
     } else {
         // ================================================ products
-        if constexpr (QT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if constexpr (QT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         // (descriptors are sums of a base and constants: in the low word, whose
         // address field does not overflow below 256 KB)
         const uint32_t base = ptx::smem_u32(smem);
