@@ -26,11 +26,6 @@ constexpr int kTile = 32;          // cached tokens per tile
 constexpr float kShift = 14.0f;    // p carries 2^14
 constexpr int kMaxSplits = 64;
 constexpr int kDirectTiles = 4;    // up to 8 rows: contexts of so many tiles go to one warp whole
-// More rows of a key head than this: the tcgen05 form.  Over 4096 INT8 tokens
-// (8 sequences, 8 key heads) it takes 47-49 us whatever the rows up to 64, the
-// warp products 32 us with 16 rows, 47 with 32, 72 with 48.
-constexpr int kWideRows = 32;
-
 // WR warps share a tile, 16 rows each; NW / WR such groups take tiles in turn.
 template <int BITS_, int D_, int WR_, int NW_>
 struct Cfg {
@@ -1306,10 +1301,25 @@ FewWarps few_warps(int head_dim) {
                           : FewWarps{FewCfg<BITS, 128>::NW, FewCfg<BITS, 128>::WORKERS};
 }
 
+// The most rows of a key head that the warps' products take; more go to the
+// tcgen05 form, whose tiles take as long for one row as for 128 and whose CTAs
+// start slowly, but which reads and converts a tile once for all of them.  Both
+// measured, 8 sequences of 4096 tokens, 8 key heads of 128, us (warps / tcgen05):
+//     16 rows   INT4 27.1 / 40.6   INT8 31.2 / 39.7   fp16 41.7 / 35.9
+//     32 rows   INT4 43.5 / 41.0   INT8 46.5 / 40.1   fp16 47.2 / 36.6
+// 32 sequences of 300 tokens, 32 rows: INT8 16.5 / 23.2.  Heads of 64, 64 rows:
+// 2 sequences of 300 tokens INT8 9.2 / 10.2, 8 of 4096 tokens 49.6 / 38.2.
+int narrow_rows(const AttentionArgs &a) {
+    const bool long_context = a.max_context >= 2048;
+    if (a.cache.head_dim == 64) return long_context ? 32 : 64;
+    if (!long_context) return 32;
+    return a.cache.kv_type == QUIK_KV_FP16 ? 8 : 16;
+}
+
 // Up to eight rows: the transposed form (wr 0), with as many workers as are
 // resident at once, or one for each tile (a tile takes a lone warp more than a
 // microsecond: one token over 200, 32 heads: 11.8 us with four tiles a worker).
-// Up to 32: one or two row warps (a warp's products have 16), and splits of the
+// More (narrow_rows): one or two row warps (a warp's products have 16), and splits of the
 // cached tokens, enough CTAs for about two a resident slot, while each warp
 // group keeps at least four tiles.
 Plan plan_of(const AttentionArgs &a) {
@@ -1320,7 +1330,7 @@ Plan plan_of(const AttentionArgs &a) {
     r.row_blocks = static_cast<int>((rows + block - 1) / block);
     const int64_t items = static_cast<int64_t>(a.sequences) * a.cache.heads * r.row_blocks;
     const int64_t tiles = (static_cast<int64_t>(a.max_context) + a.max_tokens + kTile - 1) / kTile;
-    if (rows > kWideRows) {
+    if (rows > narrow_rows(a)) {
         r.wide = rows <= 128 ? 1 : 2;
         r.row_blocks = static_cast<int>((rows + 128 * r.wide - 1) / (128 * r.wide));
         const int64_t ctas = static_cast<int64_t>(a.sequences) * a.cache.heads * r.row_blocks;

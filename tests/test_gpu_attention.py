@@ -272,6 +272,38 @@ def test_attention_split_over_the_context(bits, ctx, draft, G):
 
 
 @pytest.mark.parametrize("bits", BITS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,draft", [(3, [3, 2]), (4, [5, 1]), (1, [24, 30]), (2, [16, 9]), (4, [16, 3]), (5, [13, 1])])
+def test_attention_for_long_and_for_short_contexts(bits, D, G, draft):
+    """9 to 65 rows of a key head: the longest context that the call names chooses the
+    kernel and the number of pieces, not the result."""
+    c = Case(bits, D, 1, G, 64, [2100, 70], draft, True, seed=17)
+    for hint in (None, 100, 1 << 17):
+        c.check(hint)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,draft", [(2, 5), (3, 12), (4, 16), (2, 64)])
+def test_infinity_in_values_of_a_long_context(D, G, draft):
+    """Infinities and NaN among the drafted tokens' fp16 values, over a context for
+    which other kernels are taken than for a short one."""
+    c = Case(16, D, 1, G, 32, [2070], [draft], True, seed=19)
+    clean, _ = c.run()
+    seen = torch.zeros(draft, dtype=torch.bool)
+    for bad, x in ((1, float("inf")), (draft - 2, float("nan")), (draft // 2, -float("inf"))):
+        pos = 2070 + bad
+        c.cache.v[int(c.table[0, pos // 32]), 0, pos % 32, bad % D] = x
+        seen |= torch.from_numpy((c.mask[:, bad // 32] >> np.uint32(bad % 32)) & 1 > 0)
+    out, _ = c.run()
+    checked()
+    assert torch.equal(out[~seen], clean[~seen])
+    chan = sorted({1, draft - 2, draft // 2})
+    assert not torch.isfinite(out[seen][..., chan].float()).all(-1).any()
+    rest = [i for i in range(D) if i not in chan]
+    assert torch.equal(out[..., rest], clean[..., rest])
+
+
+@pytest.mark.parametrize("bits", BITS)
 @pytest.mark.parametrize("hint", [0, 1 << 18])
 def test_attention_rows_that_see_nothing(bits, hint):
     """No context and no bits: zeros and lse = -inf; a row that sees one token
