@@ -132,11 +132,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
     // (values broadcast from lane 0 are the same in the whole warp for the compiler
     // too: the products' descriptors and loop then live in uniform registers)
     const int lane = threadIdx.x % 32, warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);
-    const int split = blockIdx.x % p.splits, rb = blockIdx.x / p.splits;
+    const int split = blockIdx.x % p.splits;
+    const int rb = p.row_blocks - 1 - blockIdx.x / p.splits;  // (the blocks that see most start first)
     const int h = blockIdx.y, b = blockIdx.z;
-    const Seq sq = sequence(p, b, blockIdx.x == 0 && h == 0 && threadIdx.x == 0);
+    Seq sq = sequence(p, b, blockIdx.x == 0 && h == 0 && threadIdx.x == 0);
     const int rows = sq.n * p.group, row0 = rb * QT * 128;
     if (row0 >= rows) return;
+    // without a mask, what is past the block's last token is seen by none of its rows
+    if (p.mask == nullptr) sq.total = min(sq.total, sq.ctx + min(sq.n, (row0 + QT * 128 - 1) / p.group + 1));
     const int tiles = (sq.total + kTok - 1) / kTok;
     const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * split / p.splits);
     const int n = __shfl_sync(

@@ -282,6 +282,15 @@ def test_attention_for_long_and_for_short_contexts(bits, D, G, draft):
         c.check(hint)
 
 
+@pytest.mark.parametrize("bits", BITS)
+@pytest.mark.parametrize("D,G,ctx,draft", [(128, 2, [100, 0], [413, 7]), (64, 3, [70], [301]), (128, 1, [0], [257])])
+def test_chunks_of_a_prompt(bits, D, G, ctx, draft):
+    """Several blocks of rows, each of which sees the tokens up to its own last one."""
+    c = Case(bits, D, 2, G, 16, ctx, draft, False, seed=23)
+    c.check()
+    c.check(1 << 16)
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("G,draft", [(2, 5), (3, 12), (4, 16), (2, 64)])
 def test_infinity_in_values_of_a_long_context(D, G, draft):
