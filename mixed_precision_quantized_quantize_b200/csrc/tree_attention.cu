@@ -1247,25 +1247,28 @@ __global__ void __launch_bounds__(256) tree_attention_join4_kernel(const Params 
     constexpr int V = D / 32;
     float2 a[4];
     float x[4][V];
-    float M = -INFINITY;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-        const bool ok = s < p.splits;
-        a[s] = ok ? p.part_ml[s * step + row] : make_float2(-INFINITY, 0.0f);
+        if (s >= p.splits) break;
+        a[s] = p.part_ml[s * step + row];
         const float *src = p.part_o + (s * step + row) * D + lane * V;
         if constexpr (V == 4) {
-            const float4 v = ok ? *reinterpret_cast<const float4 *>(src) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const float4 v = *reinterpret_cast<const float4 *>(src);
             x[s][0] = v.x, x[s][1] = v.y, x[s][2] = v.z, x[s][3] = v.w;
         } else {
-            const float2 v = ok ? *reinterpret_cast<const float2 *>(src) : make_float2(0.0f, 0.0f);
+            const float2 v = *reinterpret_cast<const float2 *>(src);
             x[s][0] = v.x, x[s][1] = v.y;
         }
-        M = fmaxf(M, a[s].x);
     }
+    float M = -INFINITY;
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+        if (s < p.splits) M = fmaxf(M, a[s].x);
     const float base = M == -INFINITY ? 0.0f : M;
     float L = 0.0f, acc[V] = {};
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
+        if (s >= p.splits) break;
         const float f = exp2_fast(a[s].x - base);
         L = fmaf(f, a[s].y, L);
 #pragma unroll

@@ -6,20 +6,29 @@
 //     S = Q K^T    tcgen05 kind::f16, 128 x 64, both operands in shared memory
 //     p            four warps a row block, a thread a row, as in tree_attention.cu
 //     O += P V     P in tensor memory (over the S it came from), V in shared memory
-// Three loader warps bring the cached rows in by cp.async; quantised rows land in
-// a raw ring and are converted to fp16 (exact: they are integer codes) into the
-// products' operand tiles, once for both row blocks.  K and V tiles have one
-// image, [64 tokens][64 channels] blocks in the 128-byte swizzle: K is read
-// along its rows (K-major), V across them (MN-major, the transpose bit of B).
-// S is double-buffered, so the products of tile t + 1 run under the softmax of
-// tile t, and the two row blocks' softmaxes under each other's products.
+// Six loader warps bring the cached rows in by cp.async; quantised rows land in a
+// raw ring and are converted to fp16 (exact: they are integer codes) into the
+// products' operand tiles, once for both row blocks.  A warp of its own brings
+// the scales and works out their unit (by one of the loaders it made that one the
+// slowest: 64 rows of 4096 INT8 tokens 45.1 -> 41.4 us without).  K and V tiles
+// have one image, [64 tokens][64 channels] blocks in the 128-byte swizzle: K is
+// read along its rows (K-major), V across them (MN-major, the transpose bit of
+// B).  S is double-buffered, so the products of tile t + 1 run under the softmax
+// of tile t, and the two row blocks' softmaxes under each other's products.
 //
 // The running maximum is only moved when a row's scores exceed it by 5 in log2
 // (p carries 2^10 here, so p <= 2^15 < 65504): rescaling O is a trip through
 // tensor memory, and after the first tiles it hardly ever happens.
 //
-// Bound by the exponentials: 256 rows x 64 tokens take the 4 x 4 lanes of an
-// SM's special-function units 1024 cycles, the products as many.
+// 256 rows x 64 tokens take 2300 cycles.  The exponentials alone take 1024 (4 x 4
+// lanes an SM), the products about as many (Q is read from shared memory again
+// for every 64 tokens), and shared memory is busy for three quarters of the time:
+// operands, conversion and scales.  Around the tiles a CTA takes 6000 cycles to
+// its first S and 5000 for its results.  64 drafted tokens over 8 x 4096 of INT8,
+// 32 / 8 heads of 128: 55 us with the join, 17.4 by the products' rate.  Tried and slower:
+// two threads a row (more warps, the same time: 60.5 us), one row block by two
+// groups that take tiles in turn (64 rows fp16 55.0 against 38.0 us), pieces by
+// each sequence's own length (60.7 against 58.3 us: finding the place costs more).
 #include <type_traits>
 
 #include "attention.cuh"
@@ -36,7 +45,7 @@ constexpr int kTok = 64;            // cached tokens per tile
 constexpr float kLazy = 5.0f;        // how far scores may pass the running maximum (log2)
 constexpr float kWideShift = 10.0f;  // p carries 2^10
 constexpr float kJoinShift = 14.0f;  // what the join takes p to carry
-constexpr int kLoaders = 192;        // and a warp for the scales
+constexpr int kLoaders = 192;        // threads; and a warp for the scales
 
 template <int BITS_, int D_, int QT_>
 struct WideCfg {
@@ -174,6 +183,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
 
     if (warp < QT * 4) {
         // ================================================ softmax: a thread a row
+        // (8 warps of 184 registers a thread and 8 of 72 are the 16 of 128 that start)
         if constexpr (QT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         const int g = warp / 4;
         const uint32_t lanes = static_cast<uint32_t>(warp % 4) * 32 << 16;
