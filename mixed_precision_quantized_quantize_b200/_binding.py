@@ -664,14 +664,17 @@ class QuikKVCache:
         for t in (v, k_scale, v_scale):
             if t is not None and t.device != k.device:
                 raise ValueError(f"buffers on {k.device} and on {t.device}")
-        # the buffers live as long as this object does: the struct holds their addresses
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        # the buffers live as long as this object does and stay the same ones: the struct
+        # holds their addresses
+        self._buffers = k, v, k_scale, v_scale
         self.heads, self.head_dim, self.page_size, self.pages = heads, row * per, page_size, pages
         self.device, self.index = k.device, k.get_device()
         self.struct = quik_kv_cache(kind, heads, row * per, page_size, pages, 0, _ptr(k, k.dtype, "k"),
                                     _ptr(v, k.dtype, "v"), _ptr(k_scale, torch.float32, "k_scale"),
                                     _ptr(v_scale, torch.float32, "v_scale"))
         self.address = ctypes.addressof(self.struct)
+
+    k, v, k_scale, v_scale = (property(lambda self, i=i: self._buffers[i]) for i in range(4))
 
     @classmethod
     def empty(cls, pages: int, heads: int, head_dim: int, page_size: int = 64, bits: int = 16,

@@ -148,7 +148,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
     const int rows = sq.n * p.group, row0 = rb * QT * 128;
     if (row0 >= rows) return;
     // without a mask, what is past the block's last token is seen by none of its rows
-    if (p.mask == nullptr) sq.total = min(sq.total, sq.ctx + min(sq.n, (row0 + QT * 128 - 1) / p.group + 1));
+    if (p.mask == nullptr)
+        sq.total = static_cast<int>(min(static_cast<int64_t>(sq.total),
+                                        static_cast<int64_t>(sq.ctx) + (row0 + QT * 128 - 1) / p.group + 1));
     const int tiles = (sq.total + kTok - 1) / kTok;
     const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * split / p.splits);
     const int n = __shfl_sync(

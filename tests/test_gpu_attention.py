@@ -488,6 +488,27 @@ def test_indices_out_of_range_are_reported():
     checked()
 
 
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("draft,hint", [(1, 0), (1, 1 << 16), (20, 0), (40, 0), (150, 0), (150, 1 << 16)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_no_pages_and_lengths_past_all_pages(bits, draft, hint, tree):
+    """A page table without columns, and a context of 2^31 - 1: every token past the
+    pages is unseen and counted, in each form of the kernel; nothing else changes."""
+    c = Case(bits, 64, 1, 2, 16, [33, 20], [draft, draft], tree, seed=21)
+    o, _, bo, _ = c.reference()
+    c.ctx[1] = 2**31 - 1
+    out, lse = c.run(hint)
+    assert q.quik_sync_check() == q.QUIK_ERR_INVALID_ARG
+    within(out[:draft], o[:draft], bo[:draft])
+    assert not torch.isnan(out).any()
+    c.ctx[1] = 20
+    c.table = c.table[:, :0]
+    out, lse = c.run(hint)
+    assert q.quik_sync_check() == q.QUIK_ERR_INVALID_ARG
+    assert not out.any() and torch.isneginf(lse).all()
+    checked()
+
+
 def test_same_result_twice_and_on_another_stream():
     c = Case(4, 128, 4, 4, 64, [900, 333], [9, 2], True, seed=21)
     a, la = c.run(1 << 18)
