@@ -494,6 +494,9 @@ QUIK_API quik_status quik_kv_gather(const quik_kv_cache *cache, int32_t tokens,
  * are counted and quik_sync_check reports QUIK_ERR_INVALID_ARG.
  *   workspace: quik_attention_workspace_size bytes (may be NULL when that is
  *   0), the caller's; two calls that may overlap on the GPU need one each.
+ * The same call gives the same bits.  The last bits of a row depend on how the
+ * call's work is shared out, so also on max_context, on the other sequences'
+ * lengths and on the GPU's number of SMs.
  */
 typedef struct {
     int32_t tokens;      /* rows of q and out */
