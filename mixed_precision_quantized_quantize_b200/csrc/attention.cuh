@@ -27,7 +27,7 @@ struct AttnParams {
     float2 *part_ml; // [splits][tokens * q_heads]
     // up to 8 rows: pieces (workers + items of them), each 8 rows as the warps hold them
     int workers;
-    bool direct;       // each worker has an item to itself and writes its rows
+    int mode;          // who takes an item
     float4 *piece_o;   // [pieces][D / 16][32]
     float2 *piece_ml;  // [pieces][8]
     int *item_span;    // [items][2]: the workers that hold an item's first and last tile

@@ -25,7 +25,6 @@ using Params = AttnParams;
 constexpr int kTile = 32;          // cached tokens per tile
 constexpr float kShift = 14.0f;    // p carries 2^14
 constexpr int kMaxSplits = 64;
-constexpr int kDirectTiles = 4;    // up to 8 rows: contexts of so many tiles go to one warp whole
 // WR warps share a tile, 16 rows each; NW / WR such groups take tiles in turn.
 template <int BITS_, int D_, int WR_, int NW_>
 struct Cfg {
@@ -540,8 +539,13 @@ __global__ void __launch_bounds__(C::NW * 32) tree_attention_kernel(const Params
 // products, accumulators and exponentials.  P^T turns from the accumulators'
 // layout into the second product's operand by movmatrix.
 //
-// The work, tiles of all sequences, key heads and blocks of 8 rows one after
-// the other, is cut into equal runs, one a warp, whatever the sequences'
+// A token over 200 of INT8, 32 heads: 6.0 us; one of 16 sequences over up to 2048 of
+// INT4, 32 heads: 37 us with the join (16.9 by the bytes; the conversion of codes
+// keeps the ALU half busy at 16 warps an SM); one over 65536 of fp16, 64 / 8 heads:
+// 54 us (40.9 by the bytes).
+//
+// Short contexts: see FewMode.  Otherwise the work, tiles of all sequences, key heads
+// and blocks of 8 rows one after the other, is cut into equal runs, one a warp, whatever the sequences'
 // lengths: no warp waits for another, and all end together.  A run crosses
 // from one item (sequence, key head, row block) to the next without emptying
 // its ring.  What a warp finds for an item is a piece; a second kernel joins an
@@ -599,9 +603,12 @@ __device__ __forceinline__ void enter(const Params &p, Cursor &c, int b) {
     }
 }
 
-// DIRECT: a worker for each item, which writes its rows itself (short contexts,
-// where a second kernel would take as long as the first).
-template <class C, bool DIRECT>
+// Who takes an item.  Short contexts are not streamed: a second kernel would take
+// as long as the first.  Then a warp has an item to itself, or the CTA's warps
+// share one and join what they found in shared memory; both write its rows.
+enum FewMode { kStream, kWarp, kGroup };
+
+template <class C, int MODE>
 __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel(const Params p) {
     constexpr int BITS = C::BITS, D = C::D;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -611,16 +618,20 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel
     int left;  // tiles still to be issued
     Cursor at;
     at.item = 0, at.tile = 0;
-    if constexpr (DIRECT) {
-        const int per = p.heads * p.row_blocks;
-        at.b = worker / per;
+    if constexpr (MODE != kStream) {
+        const int per = p.heads * p.row_blocks, index = MODE == kWarp ? worker : blockIdx.x;
+        at.b = index / per;
         if (at.b >= p.sequences) return;
-        at.item = worker % per;
-        at.sq = sequence(p, at.b, at.item == 0 && lane == 0);
+        at.item = index % per;
+        at.sq = sequence(p, at.b, at.item == 0 && lane == 0 && (MODE == kWarp || warp == 0));
         const Load l = load_of(p, at.sq);
         if (at.item >= l.items) return;
         at.tiles = l.tiles, at.items = l.items;
         left = l.tiles;
+        if constexpr (MODE == kGroup) {
+            at.tile = static_cast<int>(static_cast<int64_t>(l.tiles) * warp / C::NW);
+            left = static_cast<int>(static_cast<int64_t>(l.tiles) * (warp + 1) / C::NW) - at.tile;
+        }
     } else {
         // ---- this worker's run: the tiles of all sequences, 32 sequences at a time
         // (the first 32 are looked at once: the usual number, and this is latency)
@@ -1023,7 +1034,7 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel
                 }
             }
         }
-        if constexpr (DIRECT) continue;
+        if constexpr (MODE != kStream) continue;
         const int64_t item = place.z * (static_cast<int64_t>(p.heads) * p.row_blocks) + place.y;
         if (lane == 0 && (place.w & 4)) p.item_span[2 * item] = worker;
         if (lane == 0 && (place.w & 8)) p.item_span[2 * item + 1] = worker;
@@ -1046,7 +1057,7 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel
             }
         }
     }
-    if constexpr (DIRECT) {
+    if constexpr (MODE == kWarp) {
         // ---- the rows, through shared memory into their order (the ring is done with)
         copy_wait<0>();
         __syncwarp();
@@ -1082,6 +1093,61 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel
                 make_uint4(half2_of(a.x, a.y), half2_of(a.z, a.w), half2_of(c.x, c.y), half2_of(c.z, c.w));
             if (lane % LANES == 0 && p.lse != nullptr) p.lse[token * p.q_heads + head] = lse[x];
         }
+    }
+    if constexpr (MODE == kGroup) {
+        // ---- every warp's rows, maxima and sums in its ring (which is done with); then
+        // a thread joins eight channels of a row
+        constexpr int PITCH = D + 4;
+        copy_wait<0>();
+        __syncwarp();
+        float *rows = reinterpret_cast<float *>(ring), *ml = rows + 8 * PITCH;
+        const float up = BITS == 16 ? 1.0f : __uint_as_float(static_cast<unsigned>(127 + R) << 23);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float sum = l[e];
+#pragma unroll
+            for (int y = 4; y < 32; y *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, y);
+            if (q8 == 0) ml[2 * (2 * q4 + e)] = m[e], ml[2 * (2 * q4 + e) + 1] = sum;
+#pragma unroll
+            for (int c = 0; c < C::MT; ++c)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    rows[(2 * q4 + e) * PITCH + (BITS == 16 ? 16 * c + 8 * x + q8 : q8 * (D / 8) + 2 * c + x)] =
+                        o[c][2 * x + e] * up;
+        }
+        __syncthreads();
+        const int blocks = first_items / p.heads, h = first_item / blocks, r0 = first_item % blocks * 8;
+        constexpr int PER = 8, LANES = D / PER;
+        static_assert(8 * LANES <= C::NW * 32, "a thread each");
+        static_assert(8 * PITCH * 4 + 64 <= C::STAGES * C::STAGE, "they fit the ring");
+        const int x = threadIdx.x / LANES, d = threadIdx.x % LANES * PER, g = r0 + x;
+        if (x >= 8 || g >= first_n * p.group) return;
+        const float *all = reinterpret_cast<const float *>(smem);
+        constexpr int STEP = C::STAGES * C::STAGE / 4;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < C::NW; ++w) M = fmaxf(M, all[w * STEP + 8 * PITCH + 2 * x]);
+        const float base = M == -INFINITY ? 0.0f : M;
+        float L = 0.0f, acc[PER] = {};
+#pragma unroll
+        for (int w = 0; w < C::NW; ++w) {
+            const float *mine = all + w * STEP;
+            const float f = exp2_fast(mine[8 * PITCH + 2 * x] - base);
+            L = fmaf(f, mine[8 * PITCH + 2 * x + 1], L);
+            const float4 a = *reinterpret_cast<const float4 *>(mine + x * PITCH + d);
+            const float4 c = *reinterpret_cast<const float4 *>(mine + x * PITCH + d + 4);
+            acc[0] = fmaf(f, a.x, acc[0]), acc[1] = fmaf(f, a.y, acc[1]);
+            acc[2] = fmaf(f, a.z, acc[2]), acc[3] = fmaf(f, a.w, acc[3]);
+            acc[4] = fmaf(f, c.x, acc[4]), acc[5] = fmaf(f, c.y, acc[5]);
+            acc[6] = fmaf(f, c.z, acc[6]), acc[7] = fmaf(f, c.w, acc[7]);
+        }
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+        const int64_t token = first + g / p.group, head = h * p.group + g % p.group;
+        *reinterpret_cast<uint4 *>(p.out + token * p.out_stride + head * D + d) =
+            make_uint4(half2_of(acc[0] * inv, acc[1] * inv), half2_of(acc[2] * inv, acc[3] * inv),
+                       half2_of(acc[4] * inv, acc[5] * inv), half2_of(acc[6] * inv, acc[7] * inv));
+        if (d == 0 && p.lse != nullptr)
+            p.lse[token * p.q_heads + head] = L == 0.0f ? -INFINITY : (M - kShift + log2f(L)) * 0.693147180559945f;
     }
 }
 
@@ -1290,7 +1356,7 @@ struct Plan {
     int wide;         // > 0: the tcgen05 form, with so many blocks of 128 rows a CTA
     int wr, row_blocks, splits;
     int workers;      // up to 8 rows: warps that share the tiles
-    bool direct;      // ... of whole items each
+    FewMode mode;     // ... and who takes an item
     int64_t pieces;
 };
 
@@ -1302,6 +1368,27 @@ template <int BITS>
 FewWarps few_warps(int head_dim) {
     return head_dim == 64 ? FewWarps{FewCfg<BITS, 64>::NW, FewCfg<BITS, 64>::WORKERS}
                           : FewWarps{FewCfg<BITS, 128>::NW, FewCfg<BITS, 128>::WORKERS};
+}
+
+// Up to eight rows: who takes an item of at most `tiles` tiles.  Times are counted
+// in tiles of 128 channels, about 0.8 us for a warp.  Measured, us, one token of
+// each sequence over (a warp an item / a CTA an item / the stream and its join):
+//     1 sequence, 32 heads of 128, INT8:     100 tokens 10.0 / 5.0 / -
+//         250 tokens - / 6.2 / 7.8, 600 tokens - / 9.3 / 8.7
+//     16 sequences, 32 heads of 128, fp16:   60 tokens 7.9 / 15.2 / -
+//         150 tokens - / 18.8 / 13.6
+//     128 sequences, 32 / 8 heads of 64, INT4: 60 tokens 5.9 / 8.4 / -
+//         250 tokens - / 12.7 / 20.8, 900 tokens - / 27.3 / 34.0
+FewMode few_mode(const AttentionArgs &a, int64_t items, int64_t tiles, const FewWarps &w) {
+    const int64_t resident = static_cast<int64_t>(sm_count()) * w.sm / w.cta, waves = (items + resident - 1) / resident;
+    if (tiles <= 4) return waves == 1 ? kGroup : kWarp;
+    if (tiles > 8 * w.cta) return kStream;  // (lengths then differ by more than the join takes)
+    const double group = static_cast<double>(waves * ((tiles + w.cta - 1) / w.cta)) +
+                         2.0 * static_cast<double>(waves - 1) * w.cta / w.sm;  // a CTA's start, unless others run
+    const double stream = static_cast<double>(items * tiles) / static_cast<double>(resident * w.cta);
+    const double rows = static_cast<double>(a.sequences) * a.q_heads * a.max_tokens;
+    const double join = (2.5 + rows / 1024.0) * (128.0 / a.cache.head_dim);
+    return group - (stream < 1.0 ? 1.0 : stream) <= join ? kGroup : kStream;
 }
 
 // The most rows of a key head that the warps' products take; more go to the
@@ -1319,9 +1406,8 @@ int narrow_rows(const AttentionArgs &a) {
     return a.cache.kv_type == QUIK_KV_FP16 ? 8 : 16;
 }
 
-// Up to eight rows: the transposed form (wr 0), with as many workers as are
-// resident at once, or one for each tile (a tile takes a lone warp more than a
-// microsecond: one token over 200, 32 heads: 11.8 us with four tiles a worker).
+// Up to eight rows: the transposed form (wr 0); streamed, with as many workers as
+// are resident at once, or one for each tile.
 // More (narrow_rows): one or two row warps (a warp's products have 16), and splits of the
 // cached tokens, enough CTAs for about two a resident slot, while each warp
 // group keeps at least four tiles.
@@ -1351,9 +1437,10 @@ Plan plan_of(const AttentionArgs &a) {
         const FewWarps w = a.cache.kv_type == QUIK_KV_INT4   ? few_warps<4>(a.cache.head_dim)
                            : a.cache.kv_type == QUIK_KV_INT8 ? few_warps<8>(a.cache.head_dim)
                                                              : few_warps<16>(a.cache.head_dim);
-        r.direct = tiles <= kDirectTiles;
-        const int64_t want = r.direct ? items : items * tiles, most = static_cast<int64_t>(sm_count()) * w.sm;
-        const int64_t ctas = ((want < most || r.direct ? want : most) + w.cta - 1) / w.cta;
+        r.mode = few_mode(a, items, tiles, w);
+        const int64_t all = r.mode == kWarp ? items : r.mode == kGroup ? items * w.cta : items * tiles;
+        const int64_t most = static_cast<int64_t>(sm_count()) * w.sm;
+        const int64_t ctas = ((all < most || r.mode != kStream ? all : most) + w.cta - 1) / w.cta;
         r.workers = w.cta * static_cast<int>(ctas < 1 ? 1 : ctas);
         r.pieces = items + r.workers;
         return r;
@@ -1368,7 +1455,7 @@ Plan plan_of(const AttentionArgs &a) {
 }
 
 size_t partial_bytes(const AttentionArgs &a, const Plan &r) {
-    if (r.direct) return 0;
+    if (r.mode != kStream) return 0;
     if (r.wide == 0 && r.wr == 0)
         return static_cast<size_t>(r.pieces) * 8 * (a.cache.head_dim * 4 + 8) +
                static_cast<size_t>(r.pieces - r.workers) * 8;
@@ -1401,11 +1488,13 @@ quik_status join_splits(const Params &p, cudaStream_t stream) {
 
 template <class C>
 quik_status run_few(const Params &p, cudaStream_t stream) {
-    void (*kernel)(Params) = p.direct ? &tree_attention_few_kernel<C, true> : &tree_attention_few_kernel<C, false>;
+    void (*kernel)(Params) = p.mode == kStream ? &tree_attention_few_kernel<C, kStream>
+                             : p.mode == kWarp ? &tree_attention_few_kernel<C, kWarp>
+                                               : &tree_attention_few_kernel<C, kGroup>;
     if (!attribute_set_once(reinterpret_cast<const void *>(kernel), C::SMEM)) return QUIK_ERR_CUDA;
     kernel<<<p.workers / C::NW, C::NW * 32, C::SMEM, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return QUIK_ERR_CUDA;
-    if (p.direct) return QUIK_OK;
+    if (p.mode != kStream) return QUIK_OK;
     // many pieces an item: more warps, so that a few rounds of loads see them all
     const int64_t items = static_cast<int64_t>(p.sequences) * p.heads * p.row_blocks;
     if (p.workers >= 48 * items) return launch_join(p, &tree_attention_few_join_kernel<C, 16>, 512, stream);
@@ -1474,7 +1563,7 @@ quik_status launch_tree_attention(const AttentionArgs &a, cudaStream_t stream) {
     p.part_ml = reinterpret_cast<float2 *>(
         a.partial + static_cast<size_t>(plan.splits) * a.tokens * a.q_heads * a.cache.head_dim);
     p.workers = plan.workers;
-    p.direct = plan.direct;
+    p.mode = plan.mode;
     p.piece_o = reinterpret_cast<float4 *>(a.partial);
     p.piece_ml = reinterpret_cast<float2 *>(a.partial + static_cast<size_t>(plan.pieces) * 8 * a.cache.head_dim);
     p.item_span = reinterpret_cast<int *>(p.piece_ml + plan.pieces * 8);

@@ -283,6 +283,29 @@ def test_attention_for_long_and_for_short_contexts(bits, D, G, draft):
 
 
 @pytest.mark.parametrize("bits", BITS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("most", [90, 230])
+def test_many_short_sequences(bits, D, most):
+    """More (sequence, key head) pairs than the GPU holds CTAs: contexts that a warp
+    takes whole and ones that a CTA takes; some sequences without new tokens."""
+    r = np.random.default_rng(most)
+    ctx, draft = r.integers(0, most, 200), r.integers(0, 3, 200)
+    ctx[7], draft[:9] = most, [2, 1, 0, 0, 1, 2, 1, 2, 0]
+    c = Case(bits, D, 4, 2, 32, ctx.tolist(), draft.tolist(), True, seed=29)
+    c.check()
+    c.check(1 << 14)
+
+
+@pytest.mark.parametrize("bits", BITS)
+@pytest.mark.parametrize("ctx", [0, 40, 150, 260, 500, 765])
+def test_one_sequence_by_the_warps_of_a_cta(bits, ctx):
+    """One token over contexts that a CTA's warps share, some with less than a tile each."""
+    for D in (64, 128):
+        Case(bits, D, 3, 4, 16, [ctx], [1], False, seed=31).check()
+        Case(bits, D, 2, 2, 64, [ctx, 1], [3, 4], True, seed=31).check()
+
+
+@pytest.mark.parametrize("bits", BITS)
 @pytest.mark.parametrize("D,G,ctx,draft", [(128, 2, [100, 0], [413, 7]), (64, 3, [70], [301]), (128, 1, [0], [257])])
 def test_chunks_of_a_prompt(bits, D, G, ctx, draft):
     """Several blocks of rows, each of which sees the tokens up to its own last one."""
