@@ -262,10 +262,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
                 for (int i = 0; i < 64; ++i)
                     if (!((see[i / 32] >> (i % 32)) & 1u)) s[i] = 0xff800000u;
             }
-            float top = -INFINITY;
+            float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // (four short chains, not one)
 #pragma unroll
             for (int i = 0; i < 64; i += 2)
-                top = fmaxf(fmaxf(top, __uint_as_float(s[i])), __uint_as_float(s[i + 1]));
+                tops[i / 2 % 4] = fmaxf(fmaxf(tops[i / 2 % 4], __uint_as_float(s[i])), __uint_as_float(s[i + 1]));
+            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
             // ---- move the maximum and the unit of the values' scales only where they must
             const bool move = top > m + kLazy || (m == -INFINITY && top > -INFINITY);
             const int unit = BITS == 16 ? R : info.w;
