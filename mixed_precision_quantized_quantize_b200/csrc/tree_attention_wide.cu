@@ -222,15 +222,23 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
             const int stage = t % C::STAGES, buf = t & 1;
             const uint8_t *meta = smem + C::OFF_META + stage * C::META;
             // (the tile's scales and masks come from the loaders, S from the products)
-            alive = all_of(wide_wait(&bars->kv_full[stage], (t / C::STAGES) & 1, abort) &&
-                           wide_wait(&bars->s_full[g][buf], (t >> 1) & 1, abort));
+            // Both are done as a rule: asked for together, the answers' latencies overlap.
+            const bool kv = ptx::mbar_try_wait(&bars->kv_full[stage], (t / C::STAGES) & 1);
+            const bool sc = ptx::mbar_try_wait(&bars->s_full[g][buf], (t >> 1) & 1);
+            alive = all_of((kv || wide_wait(&bars->kv_full[stage], (t / C::STAGES) & 1, abort)) &&
+                           (sc || wide_wait(&bars->s_full[g][buf], (t >> 1) & 1, abort)));
             if (!alive) break;
             ptx::tc_fence_after();
             uint32_t s[64];
+            float4 ks[BITS == 16 ? 1 : 16];
             {
                 uint32_t lo[32], hi[32];
                 ptx::tmem_ld_32x32b_x32(s_col(g, buf) + lanes, lo);
                 ptx::tmem_ld_32x32b_x32(s_col(g, buf) + lanes + 32, hi);
+                if constexpr (BITS != 16) {  // the keys' scales come meanwhile
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) ks[i] = *reinterpret_cast<const float4 *>(meta + 16 * i);
+                }
                 ptx::tmem_ld_wait();
 #pragma unroll
                 for (int i = 0; i < 32; ++i) s[i] = lo[i], s[32 + i] = hi[i];
@@ -243,8 +251,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
             for (int i = 0; i < 16; ++i) {
                 uint64_t k0 = sc2, k1 = sc2;
                 if constexpr (BITS != 16) {
-                    const float4 k4 = *reinterpret_cast<const float4 *>(meta + 16 * i);
-                    k0 = ptx::f2(k4.x, k4.y), k1 = ptx::f2(k4.z, k4.w);
+                    k0 = ptx::f2(ks[i].x, ks[i].y), k1 = ptx::f2(ks[i].z, ks[i].w);
                 }
                 float x, y;
                 ptx::f2_split(ptx::f2_mul(ptx::f2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), k0), x, y);
