@@ -1395,10 +1395,10 @@ FewMode few_mode(const AttentionArgs &a, int64_t items, int64_t tiles, const Few
 // tcgen05 form, whose tiles take as long for one row as for 128 and whose CTAs
 // start slowly, but which reads and converts a tile once for all of them.  Both
 // measured, 8 sequences of 4096 tokens, 8 key heads of 128, us (warps / tcgen05):
-//     16 rows   INT4 27.1 / 40.6   INT8 31.2 / 39.7   fp16 41.7 / 35.9
-//     32 rows   INT4 43.5 / 41.0   INT8 46.5 / 40.1   fp16 47.2 / 36.6
-// 32 sequences of 300 tokens, 32 rows: INT8 16.5 / 23.2.  Heads of 64, 64 rows:
-// 2 sequences of 300 tokens INT8 9.2 / 10.2, 8 of 4096 tokens 49.6 / 38.2.
+//     16 rows   INT4 27.1 / 40.7   INT8 31.3 / 37.7   fp16 41.7 / 34.3
+//     32 rows   INT4 43.5 / 41.1   INT8 46.6 / 37.9   fp16 47.1 / 34.6
+// 32 sequences of 300 tokens, 32 rows: INT8 16.5 / 23.1.  Heads of 64, 64 rows:
+// 2 sequences of 300 tokens INT8 9.3 / 9.9, 8 of 4096 tokens 50.0 / 36.1.
 int narrow_rows(const AttentionArgs &a) {
     const bool long_context = a.max_context >= 2048;
     if (a.cache.head_dim == 64) return long_context ? 32 : 64;

@@ -20,12 +20,14 @@
 // (p carries 2^10 here, so p <= 2^15 < 65504): rescaling O is a trip through
 // tensor memory, and after the first tiles it hardly ever happens.
 //
-// 256 rows x 64 tokens take 2300 cycles.  The exponentials alone take 1024 (4 x 4
-// lanes an SM), the products about as many (Q is read from shared memory again
-// for every 64 tokens), and shared memory is busy for three quarters of the time:
-// operands, conversion and scales.  Around the tiles a CTA takes 6000 cycles to
-// its first S and 5000 for its results.  64 drafted tokens over 8 x 4096 of INT8,
-// 32 / 8 heads of 128: 55 us with the join, 17.4 by the products' rate.  Tried and slower:
+// 256 rows x 64 tokens take 2300 to 2400 cycles, in which the softmax warps, two
+// beside each other on a quarter of the SM, are never idle: 200 for the wait, 550
+// to 900 to the maximum, 1400 for the exponentials (1024 of them the rate of the
+// special-function units for both), 100 for P.  The products take 900 and the
+// conversion 1800, beside them.  Around the tiles a CTA takes 6000 cycles to its
+// first S and 5000 for its results.  64 drafted tokens over 8 x 4096 of INT8,
+// 32 / 8 heads of 128: 55 us with the join, 17.4 by the products' rate.  A chunk of
+// 2048 tokens of a prompt, fp16: 95 us.  Tried and slower:
 // two threads a row (more warps, the same time: 60.5 us), one row block by two
 // groups that take tiles in turn (64 rows fp16 55.0 against 38.0 us), pieces by
 // each sequence's own length (60.7 against 58.3 us: finding the place costs more).
