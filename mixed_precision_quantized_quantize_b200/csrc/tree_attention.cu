@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(C::NW * 32) tree_attention_kernel(const Params
 // products, accumulators and exponentials.  P^T turns from the accumulators'
 // layout into the second product's operand by movmatrix.
 //
-// A token over 200 of INT8, 32 heads: 6.0 us; one of 16 sequences over up to 2048 of
+// A token over 200 of INT8, 32 heads: 6.4 us; one of 16 sequences over up to 2048 of
 // INT4, 32 heads: 37 us with the join (16.9 by the bytes; the conversion of codes
 // keeps the ALU half busy at 16 warps an SM); one over 65536 of fp16, 64 / 8 heads:
 // 54 us (40.9 by the bytes).
@@ -741,6 +741,11 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel
     uint32_t qf[C::STEPS][2];  // the query rows as the products' second operand
     int tok[2], first = 0;     // new token of rows 2 q4, 2 q4 + 1; the sequence's first row
     float o[C::MT][4], m[2], l[2];
+    // Of p as it enters the product (with the values' scale): what its rounding added,
+    // and its sum before that, one half a row.  Kept for short contexts, where a row
+    // may see a token or two (20 of a tile's 750 instructions).
+    constexpr bool MEND = MODE != kStream;
+    uint64_t added = 0, exact = 0;
     int R = 0;
 
     // A new item: this lane's query row is q8, and of it the channels that the
@@ -788,11 +793,30 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel
             tok[e] = x < rows ? x / p.group : -1;
             m[e] = -INFINITY, l[e] = 0.0f;
         }
+        added = exact = 0;
         R = -100;
 #pragma unroll
         for (int i = 0; i < C::MT; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
+    };
+    // The factor that takes the roundings' common part out of row e's O: a token that
+    // has most of the weight would else give its own rounding to the whole row (three
+    // tokens: 1.6 times the error of the output's rounding alone).  Weights of one
+    // sign have theirs within 2^-11; anything else is left as it is.
+    auto mend = [&](int e, float sum) {
+        float d, w, other;
+        if (e == 0)
+            ptx::f2_split(added, d, other), ptx::f2_split(exact, w, other);
+        else
+            ptx::f2_split(added, other, d), ptx::f2_split(exact, other, w);
+#pragma unroll
+        for (int y = 4; y < 32; y *= 2) {
+            d += __shfl_xor_sync(0xffffffffu, d, y);
+            if constexpr (BITS != 16) w += __shfl_xor_sync(0xffffffffu, w, y);
+        }
+        if constexpr (BITS == 16) w = sum;
+        return w > 0.0f && fabsf(d) <= w * 0x1p-10f ? w / (w + d) : 1.0f;
     };
     // (of the first item while its first tile is on the way)
     open(first_b, first_item);
@@ -920,6 +944,8 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel
 #pragma unroll
                 for (int j = 0; j < 4; ++j) o[i][j] *= alpha[j & 1];
         }
+        if constexpr (MEND) added = ptx::f2_mul(added, ptx::f2(alpha[0], alpha[1]));
+        if constexpr (MEND && BITS != 16) exact = ptx::f2_mul(exact, ptx::f2(alpha[0], alpha[1]));
         // ---- p, transposed into the second operand
         uint32_t pf[2][2];
 #pragma unroll
@@ -937,7 +963,14 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel
                         if (masked && !((see[e] >> (16 * i + 8 * f + q8)) & 1u)) x[e] = 0.0f;
                     }
                 }
-                pf[i][f] = transpose8(half2_of(x[0], x[1]));
+                const __half2 h2 = __floats2half2_rn(x[0], x[1]);
+                if constexpr (MEND) {
+                    const float2 r = __half22float2(h2);
+                    const uint64_t x2 = ptx::f2(x[0], x[1]);
+                    added = ptx::f2_add(added, ptx::f2_sub(ptx::f2(r.x, r.y), x2));
+                    if constexpr (BITS != 16) exact = ptx::f2_add(exact, x2);
+                }
+                pf[i][f] = transpose8(*reinterpret_cast<const uint32_t *>(&h2));
             }
         // ---- O^T += V^T P^T
         if constexpr (BITS == 16) {
@@ -1069,7 +1102,7 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel
             float sum = l[e];
 #pragma unroll
             for (int y = 4; y < 32; y *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, y);
-            const float f = sum == 0.0f ? 0.0f : up / sum;
+            const float f = (sum == 0.0f ? 0.0f : up / sum) * mend(e, sum);
             if (q8 == 0)
                 lse[2 * q4 + e] = sum == 0.0f ? -INFINITY : (m[e] - kShift + log2f(sum)) * 0.693147180559945f;
 #pragma unroll
@@ -1107,13 +1140,14 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel
             float sum = l[e];
 #pragma unroll
             for (int y = 4; y < 32; y *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, y);
+            const float f = up * mend(e, sum);
             if (q8 == 0) ml[2 * (2 * q4 + e)] = m[e], ml[2 * (2 * q4 + e) + 1] = sum;
 #pragma unroll
             for (int c = 0; c < C::MT; ++c)
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
                     rows[(2 * q4 + e) * PITCH + (BITS == 16 ? 16 * c + 8 * x + q8 : q8 * (D / 8) + 2 * c + x)] =
-                        o[c][2 * x + e] * up;
+                        o[c][2 * x + e] * f;
         }
         __syncthreads();
         const int blocks = first_items / p.heads, h = first_item / blocks, r0 = first_item % blocks * 8;

@@ -296,6 +296,22 @@ def test_many_short_sequences(bits, D, most):
     c.check(1 << 14)
 
 
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("D", [64, 128])
+def test_one_visible_token_is_its_value(bits, D):
+    """A row that sees one token alone: the weight's own rounding cancels, and the output
+    is that token's value, rounded once.  (The sums and the quotient take a few steps of
+    2^-24, so it may fall on the other side of a tie: one step of fp16 at most.)"""
+    c = Case(bits, D, 4, 1, 16, [0] * 40, [1] * 40, False, seed=37)
+    out, _ = c.run()
+    checked()
+    v = ref.values(c.cache.v.cpu().numpy(), c.cache.v_scale.cpu().numpy(), bits)
+    want = np.stack([v[c.table[b, 0], :, 0] for b in range(40)])
+    got = out.cpu().numpy().astype(np.float64)
+    step = np.spacing(np.abs(want).astype(np.float16)).astype(np.float64)
+    assert (np.abs(got - want) <= step * (0.5 + 2.0 ** -9)).all()
+
+
 @pytest.mark.parametrize("bits", BITS)
 @pytest.mark.parametrize("ctx", [0, 40, 150, 260, 500, 765])
 def test_one_sequence_by_the_warps_of_a_cta(bits, ctx):
