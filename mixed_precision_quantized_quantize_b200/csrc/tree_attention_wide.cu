@@ -185,10 +185,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
     const auto s_col = [&](int g, int buf) { return tmem + (g * 2 + buf) * kTok; };
     const auto o_col = [&](int g) { return tmem + QT * 2 * kTok + g * D; };
 
+    // 8 warps of 184 registers a thread and 8 of 72 are the 16 of 128 that start.
+    // All four warps of a warpgroup have to meet the same instruction, and the last
+    // one's belong to two roles: so it comes before the roles part.
+    if constexpr (QT == 2) {
+        if (warp < QT * 4)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    }
     if (warp < QT * 4) {
         // ================================================ softmax: a thread a row
-        // (8 warps of 184 registers a thread and 8 of 72 are the 16 of 128 that start)
-        if constexpr (QT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         const int g = warp / 4;
         const uint32_t lanes = static_cast<uint32_t>(warp % 4) * 32 << 16;
         const int row = row0 + g * 128 + warp % 4 * 32 + lane;
@@ -484,7 +491,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
             }
         }
     } else if (warp < MMA_WARP) {
-        if constexpr (QT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         // ================================================ loaders
         const int lt = threadIdx.x - QT * 128;
         // a thread's chunks of K (and V): the same place in rows TSTEP apart
@@ -719,7 +725,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
         copy_wait<0>();
     } else {
         // ================================================ products
-        if constexpr (QT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         // (descriptors are sums of a base and constants: in the low word, whose
         // address field does not overflow below 256 KB)
         const uint32_t base = ptx::smem_u32(smem);

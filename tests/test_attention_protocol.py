@@ -3,9 +3,13 @@ issuer of the products, two softmax groups) as the sequences of waits, arrivals
 and stage uses that their code makes, under random schedules.  Every schedule
 has to end, no role may use a stage that another still owns, and a wait by
 parity has to mean the phase it was written for."""
+import os
 import random
+import re
 
 import pytest
+
+import mixed_precision_quantized_quantize_b200 as q
 
 
 class Barrier:
@@ -133,3 +137,23 @@ def test_a_wait_for_the_wrong_phase_is_seen():
     with pytest.raises(AssertionError):
         for seed in range(60):
             simulate(8, 3, 0, seed, last_waits=False)
+
+
+def test_a_warpgroup_meets_one_register_instruction():
+    """setmaxnreg is for a whole warpgroup: all of its warps have to meet the same
+    instruction, whatever their roles.  So there is one to take registers and one to
+    give them back, before the roles part, and what is taken was there at the launch."""
+    with open(os.path.join(os.path.dirname(q.LIB_PATH), "csrc", "tree_attention_wide.cu")) as f:
+        text = f.read()
+    code = re.sub(r"//[^\n]*", "", text)
+    sites = [(m.start(), m.group(1), int(m.group(2)))
+             for m in re.finditer(r"setmaxnreg\.(inc|dec)\.sync\.aligned\.u32 (\d+);", code)]
+    assert [s[1] for s in sites] == ["inc", "dec"]
+    roles = code.index("s_col(g, buf) + lanes")  # the first line that only one role runs
+    assert all(s[0] < roles for s in sites) and code.rindex("if (warp", 0, roles) > sites[1][0]
+    # two row blocks: 8 softmax warps, 6 loaders, one for the scales, one for the products
+    blocks, loaders = 2, int(re.search(r"kLoaders = (\d+);", code).group(1))
+    softmax, others = blocks * 128, loaders + 64
+    assert softmax % 128 == 0 and others % 128 == 0  # whole warpgroups on either side
+    at_launch = 65536 // (softmax + others)
+    assert softmax * sites[0][2] + others * sites[1][2] <= (softmax + others) * at_launch
