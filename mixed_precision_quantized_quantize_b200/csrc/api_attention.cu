@@ -101,6 +101,10 @@ quik_status quik_qk_norm_rope(const quik_heads *heads, const void *q, int64_t q_
     quik_status st = check_heads(heads);
     if (st != QUIK_OK) return st;
     if (heads->q_heads + heads->kv_heads == 0) return QUIK_ERR_INVALID_ARG;
+    // nothing of a side without heads is used (the kernel takes the lanes past the
+    // last row for rows of k, and would read its weight)
+    if (heads->q_heads == 0) q_gamma = nullptr;
+    if (heads->kv_heads == 0) k_gamma = nullptr;
     if ((q_gamma != nullptr || k_gamma != nullptr) && !(std::isfinite(eps) && eps > 0.0f))
         return QUIK_ERR_INVALID_ARG;
     if ((q_gamma != nullptr && !aligned(q_gamma, 16)) || (k_gamma != nullptr && !aligned(k_gamma, 16)))

@@ -60,6 +60,17 @@ def test_qk_norm_rope_refusals(L):
         assert qk(L, heads(), **bad) == q.QUIK_ERR_INVALID_ARG, bad
 
 
+def test_qk_norm_rope_looks_at_nothing_of_no_heads(L):
+    """Without query or key heads that side's pointers are not used: neither checked
+    (nor, in the kernel, read)."""
+    for none, bad in ((dict(kv_heads=0), dict(kp=ODD, ks=3, kg=ODD, ko=ODD, kos=-1)),
+                      (dict(q_heads=0), dict(qp=ODD, qs=3, qg=ODD, qo=ODD, qos=-1))):
+        # eps belongs to the weights in use: there are none
+        assert qk(L, heads(tokens=0, **none), eps=0.0, **bad) == q.QUIK_OK
+    assert qk(L, heads(kv_heads=0), kg=ODD, qp=ODD) == q.QUIK_ERR_INVALID_ARG
+    assert qk(L, heads(kv_heads=0), qg=G, kg=ODD, eps=0.0) == q.QUIK_ERR_INVALID_ARG
+
+
 def append(L, h, c, kp=G, ks=256, vp=G, vs=256, cos=G, sin=G, pos=G, slots=G):
     return L.quik_kv_append(None if h is None else ctypes.byref(h), None if c is None else ctypes.byref(c), kp, ks,
                             vp, vs, cos, sin, pos, slots, None)
