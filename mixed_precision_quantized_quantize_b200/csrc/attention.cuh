@@ -180,6 +180,10 @@ __device__ __forceinline__ unsigned seen(const AttnParams &p, int first, int tok
 __device__ __forceinline__ int top_exponent(unsigned top) {
     return min(max(static_cast<int>(top >> 23) - 126, -100), 126);
 }
+// 2^-R, for R from -126 to 126.
+__device__ __forceinline__ float unit_of(int R) { return __uint_as_float(static_cast<unsigned>(127 - R) << 23); }
+// 1 / u of such a power of two.
+__device__ __forceinline__ float inverse_unit(float u) { return __uint_as_float((254u << 23) - __float_as_uint(u)); }
 __device__ __forceinline__ unsigned finite_bits(float x) {
     const unsigned u = __float_as_uint(x) & 0x7fffffffu;
     return u < 0x7f800000u ? u : 0u;

@@ -12,9 +12,10 @@
 // with V; the factor 2^14 (it cancels in O / l) keeps p's far below the maximum
 // out of fp16's subnormal range, and p <= 2^14 stays below its largest value.
 // Quantised values enter the product as their integer codes, exact in fp16;
-// their scale multiplies p in fp32 before that rounding, relative to a running
-// power of two 2^R above every scale met so far (O then is in units of 2^R), so
-// p stays within fp16 whatever the scales are.
+// their scale multiplies p in fp32 before that rounding, relative to a row's running
+// power of two 2^R above every scale that the row has seen so far (its O then is
+// in units of 2^R), so p stays within fp16 whatever the scales are, and a token
+// that the row does not see has no part in it.
 #include "attention.cuh"
 
 namespace quik {
@@ -25,6 +26,7 @@ using Params = AttnParams;
 constexpr int kTile = 32;          // cached tokens per tile
 constexpr float kShift = 14.0f;    // p carries 2^14
 constexpr int kMaxSplits = 64;
+constexpr float kFirstUnit = 0x1p100f;  // 2^-R, no scale seen yet
 // WR warps share a tile, 16 rows each; NW / WR such groups take tiles in turn.
 template <int BITS_, int D_, int WR_, int NW_>
 struct Cfg {
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(C::NW * 32) tree_attention_kernel(const Params
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-    int R = -100;  // exponent of the unit of o (quantised values)
+    float unit[2] = {kFirstUnit, kFirstUnit};  // of o's rows, 2^-R (quantised values)
 
     int next = t0 + tg;  // tile to be issued next, and its pages
     int id = src.page_of(next);
@@ -356,26 +358,40 @@ __global__ void __launch_bounds__(C::NW * 32) tree_attention_kernel(const Params
             l[e] *= alpha[e];
             base[e] -= kShift;
         }
-        // ---- the unit of the values' scales
-        float unit = 1.0f;
+        // ---- the rows' units of the values' scales
         if constexpr (BITS != 16) {
-            // only a scale above the unit (or one that is not finite) has a closer look
-            unit = __uint_as_float(static_cast<unsigned>(127 - R) << 23);
+            // only a scale above a unit (or one that is not finite) has a closer look
             float big = 0.0f;
 #pragma unroll
             for (int n = 0; n < 4; ++n) big = fmaxf(fmaxf(big, fabsf(vsc[n][0])), fabsf(vsc[n][1]));
-            if (__any_sync(0xffffffffu, big * unit > 1.0f)) {
-                unsigned top = 0;  // largest finite magnitude, by its bits
+            if (__any_sync(0xffffffffu, big * fmaxf(unit[0], unit[1]) > 1.0f)) {
+                unsigned top[2] = {0, 0};  // largest finite magnitudes that the rows see, by their bits
 #pragma unroll
-                for (int n = 0; n < 4; ++n) top = max(top, max(finite_bits(vsc[n][0]), finite_bits(vsc[n][1])));
-                const int e = top_exponent(__reduce_max_sync(0xffffffffu, top));
-                if (e > R) {
-                    const float f = exp2_fast(static_cast<float>(R - e));
-                    alpha[0] *= f, alpha[1] *= f;
-                    R = e;
+                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const unsigned u = finite_bits(vsc[n][j]), bit = 8 * n + 2 * q4 + j;
+                        top[0] = max(top[0], (see[0] >> bit) & 1u ? u : 0u);
+                        if (masked) top[1] = max(top[1], (see[1] >> bit) & 1u ? u : 0u);
+                    }
+                if (masked) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        top[e] = max(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+                        top[e] = max(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+                    }
+                } else {  // (all rows see all of it)
+                    top[0] = top[1] = __reduce_max_sync(0xffffffffu, top[0]);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float u = unit_of(top_exponent(top[e]));
+                    if (u < unit[e]) {
+                        alpha[e] *= u * inverse_unit(unit[e]);
+                        unit[e] = u;
+                    }
                 }
             }
-            unit = __uint_as_float(static_cast<unsigned>(127 - R) << 23);
         }
         if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
 #pragma unroll
@@ -395,9 +411,11 @@ __global__ void __launch_bounds__(C::NW * 32) tree_attention_kernel(const Params
                 l[j >> 1] += x[j];
             }
             if constexpr (BITS != 16) {
-                const float a = vsc[n][0] * unit, c = vsc[n][1] * unit;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] *= j & 1 ? c : a;
+                for (int e = 0; e < 2; ++e)
+                    ptx::f2_split(ptx::f2_mul(ptx::f2(x[2 * e], x[2 * e + 1]),
+                                              ptx::f2_mul(ptx::f2(vsc[n][0], vsc[n][1]), ptx::f2(unit[e], unit[e]))),
+                                  x[2 * e], x[2 * e + 1]);
                 if (masked) {  // an unseen token's scale may be anything
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
@@ -509,9 +527,9 @@ __global__ void __launch_bounds__(C::NW * 32) tree_attention_kernel(const Params
     __syncthreads();
     float *mo = reinterpret_cast<float *>(smem) + warp * 16 * C::OP;
     float2 *ml = reinterpret_cast<float2 *>(smem + C::NW * 16 * C::OP * 4);
-    const float up = BITS == 16 ? 1.0f : __uint_as_float(static_cast<unsigned>(127 + R) << 23);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
+        const float up = BITS == 16 ? 1.0f : inverse_unit(unit[e]);
         l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
         l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
         if (q4 == 0) ml[warp * 16 + q8 + 8 * e] = make_float2(m[e], l[e]);
@@ -746,7 +764,7 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel
     // may see a token or two (20 of a tile's 750 instructions).
     constexpr bool MEND = MODE != kStream;
     uint64_t added = 0, exact = 0;
-    int R = 0;
+    float unit[2];  // of O's rows, 2^-R (quantised values)
 
     // A new item: this lane's query row is q8, and of it the channels that the
     // lanes' K words give up together.
@@ -794,7 +812,7 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel
             m[e] = -INFINITY, l[e] = 0.0f;
         }
         added = exact = 0;
-        R = -100;
+        unit[0] = unit[1] = kFirstUnit;
 #pragma unroll
         for (int i = 0; i < C::MT; ++i)
 #pragma unroll
@@ -920,23 +938,38 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel
             l[e] *= alpha[e];
             base[e] -= kShift;
         }
-        float unit = 1.0f;
+        // ---- the rows' units of the values' scales
         if constexpr (BITS != 16) {
-            // only a scale above the unit (or one that is not finite) has a closer look
-            unit = __uint_as_float(static_cast<unsigned>(127 - R) << 23);
+            // only a scale above a unit (or one that is not finite) has a closer look
             const float big = fmaxf(fmaxf(fabsf(vsc[0][0]), fabsf(vsc[0][1])),
                                     fmaxf(fabsf(vsc[1][0]), fabsf(vsc[1][1])));
-            if (__any_sync(0xffffffffu, big * unit > 1.0f)) {
-                const unsigned top = max(max(finite_bits(vsc[0][0]), finite_bits(vsc[0][1])),
-                                         max(finite_bits(vsc[1][0]), finite_bits(vsc[1][1])));
-                const int e = top_exponent(__reduce_max_sync(0xffffffffu, top));
-                if (e > R) {
-                    const float f = exp2_fast(static_cast<float>(R - e));
-                    alpha[0] *= f, alpha[1] *= f;
-                    R = e;
+            if (__any_sync(0xffffffffu, big * fmaxf(unit[0], unit[1]) > 1.0f)) {
+                unsigned top[2] = {0, 0};  // largest finite magnitudes that the rows see, by their bits
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        const unsigned u = finite_bits(vsc[i][f]), bit = 16 * i + 8 * f + q8;
+                        top[0] = max(top[0], (see[0] >> bit) & 1u ? u : 0u);
+                        if (masked) top[1] = max(top[1], (see[1] >> bit) & 1u ? u : 0u);
+                    }
+                if (masked) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int y = 4; y < 32; y *= 2) top[e] = max(top[e], __shfl_xor_sync(0xffffffffu, top[e], y));
+                } else {  // (all rows see all of it)
+                    top[0] = top[1] = __reduce_max_sync(0xffffffffu, top[0]);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float u = unit_of(top_exponent(top[e]));
+                    if (u < unit[e]) {
+                        alpha[e] *= u * inverse_unit(unit[e]);
+                        unit[e] = u;
+                    }
                 }
             }
-            unit = __uint_as_float(static_cast<unsigned>(127 - R) << 23);
         }
         if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
 #pragma unroll
@@ -957,11 +990,14 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel
                 for (int e = 0; e < 2; ++e) {
                     x[e] = exp2_fast(s[i][2 * f + e] - base[e]);
                     l[e] += x[e];
-                    if constexpr (BITS != 16) {
-                        x[e] *= vsc[i][f] * unit;
-                        // an unseen token's scale may be anything
+                }
+                if constexpr (BITS != 16) {
+                    ptx::f2_split(ptx::f2_mul(ptx::f2(x[0], x[1]), ptx::f2_mul(ptx::f2(vsc[i][f], vsc[i][f]),
+                                                                               ptx::f2(unit[0], unit[1]))),
+                                  x[0], x[1]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)  // an unseen token's scale may be anything
                         if (masked && !((see[e] >> (16 * i + 8 * f + q8)) & 1u)) x[e] = 0.0f;
-                    }
                 }
                 const __half2 h2 = __floats2half2_rn(x[0], x[1]);
                 if constexpr (MEND) {
@@ -1074,12 +1110,13 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel
         if (place.w & 2) {
             // ---- the piece, as the lanes hold it; rows that do not exist are left out
             const int64_t piece = worker + item;
-            const float up = BITS == 16 ? 1.0f : __uint_as_float(static_cast<unsigned>(127 + R) << 23);
+            const float up0 = BITS == 16 ? 1.0f : inverse_unit(unit[0]);
+            const float up1 = BITS == 16 ? 1.0f : inverse_unit(unit[1]);
             float4 *dst = p.piece_o + piece * (C::MT * 32) + lane;
             if (tok[0] >= 0) {
 #pragma unroll
                 for (int c = 0; c < C::MT; ++c)
-                    dst[c * 32] = make_float4(o[c][0] * up, o[c][1] * up, o[c][2] * up, o[c][3] * up);
+                    dst[c * 32] = make_float4(o[c][0] * up0, o[c][1] * up1, o[c][2] * up0, o[c][3] * up1);
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -1096,9 +1133,9 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel
         __syncwarp();
         static_assert(8 * (D + 4) * 4 + 32 <= C::STAGES * C::STAGE, "the rows fit the warp's ring");
         float *rows = reinterpret_cast<float *>(ring), *lse = rows + 8 * (D + 4);
-        const float up = BITS == 16 ? 1.0f : __uint_as_float(static_cast<unsigned>(127 + R) << 23);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+            const float up = BITS == 16 ? 1.0f : inverse_unit(unit[e]);
             float sum = l[e];
 #pragma unroll
             for (int y = 4; y < 32; y *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, y);
@@ -1134,9 +1171,9 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) tree_attention_few_kernel
         copy_wait<0>();
         __syncwarp();
         float *rows = reinterpret_cast<float *>(ring), *ml = rows + 8 * PITCH;
-        const float up = BITS == 16 ? 1.0f : __uint_as_float(static_cast<unsigned>(127 + R) << 23);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+            const float up = BITS == 16 ? 1.0f : inverse_unit(unit[e]);
             float sum = l[e];
 #pragma unroll
             for (int y = 4; y < 32; y *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, y);

@@ -48,6 +48,7 @@ constexpr float kLazy = 5.0f;        // how far scores may pass the running maxi
 constexpr float kWideShift = 10.0f;  // p carries 2^10
 constexpr float kJoinShift = 14.0f;  // what the join takes p to carry
 constexpr int kLoaders = 192;        // threads; and a warp for the scales
+constexpr int kOwnUnit = 512;        // marks a tile whose scales' unit goes by the row (added to -100 .. 126)
 
 template <int BITS_, int D_, int QT_>
 struct WideCfg {
@@ -112,6 +113,9 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t addr, uint32_t block_bytes)
     return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)(block_bytes >> 4) << 16) |
            ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
+
+// The exponent of the unit when a scale's is e: with some room, so that it moves less often.
+__device__ __forceinline__ int raised(int R, int e) { return e > R ? min(e + 1, 126) : R; }
 
 // One lane of a converged warp, the same one every time.
 __device__ __forceinline__ bool elect_one() {
@@ -270,7 +274,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
                 s[4 * i + 2] = __float_as_uint(x), s[4 * i + 3] = __float_as_uint(y);
             }
             unsigned see[2] = {static_cast<unsigned>(info.x), static_cast<unsigned>(info.y)};
-            const bool masked = (see[0] & see[1]) != 0xffffffffu || j0 + kTok > 0;
+            const bool own = BITS != 16 && info.w > 126;  // (rows see the tile each in their way)
+            const bool masked = (see[0] & see[1]) != 0xffffffffu || (BITS == 16 ? j0 + kTok > 0 : own);
             if (masked) {
                 see[0] &= seen(p, sq.first, tok, j0);
                 see[1] &= seen(p, sq.first, tok, j0 + 32);
@@ -285,8 +290,25 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
             const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
             // ---- move the maximum and the unit of the values' scales only where they must
             const bool move = top > m + kLazy || (m == -INFINITY && top > -INFINITY);
-            const int unit = BITS == 16 ? R : info.w;
-            if (__any_sync(0xffffffffu, move) || unit != R) {
+            int unit = R;
+            if constexpr (BITS != 16) {
+                if (!own) {
+                    unit = info.w;
+                } else if (info.w - kOwnUnit > R) {
+                    // a scale above this row's unit, which the row may not see
+                    unsigned most = 0;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float4 v4 = *reinterpret_cast<const float4 *>(meta + kTok * 4 + 16 * i);
+                        const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if ((see[i / 8] >> (4 * i % 32 + j)) & 1u) most = max(most, finite_bits(v[j]));
+                    }
+                    unit = raised(R, top_exponent(most));
+                }
+            }
+            if (__any_sync(0xffffffffu, move || unit != R)) {
                 const float to = move ? top : m;
                 float alpha = move ? (m == -INFINITY ? 0.0f : exp2_fast(m - to)) : 1.0f;
                 l *= alpha;
@@ -311,6 +333,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
             // ---- p
             const float base = (m == -INFINITY ? 0.0f : m) - kWideShift;
             const uint64_t b2 = ptx::f2(base, base);
+            // what the scales as they stand in shared memory still lack
+            const float rest = own ? unit_of(R) : 1.0f;
+            const uint64_t rest2 = ptx::f2(rest, rest);
             uint64_t sum = 0;
             uint32_t pk[32];
             auto weights = [&](auto some) {
@@ -326,8 +351,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
                     sum = ptx::f2_add(sum, ptx::f2_add(ptx::f2(x[0], x[1]), ptx::f2(x[2], x[3])));
                     if constexpr (BITS != 16) {
                         const float4 v4 = *reinterpret_cast<const float4 *>(meta + kTok * 4 + 16 * i);
-                        ptx::f2_split(ptx::f2_mul(ptx::f2(x[0], x[1]), ptx::f2(v4.x, v4.y)), x[0], x[1]);
-                        ptx::f2_split(ptx::f2_mul(ptx::f2(x[2], x[3]), ptx::f2(v4.z, v4.w)), x[2], x[3]);
+                        uint64_t v0 = ptx::f2(v4.x, v4.y), v1 = ptx::f2(v4.z, v4.w);
+                        if constexpr (decltype(some)::value) v0 = ptx::f2_mul(v0, rest2), v1 = ptx::f2_mul(v1, rest2);
+                        ptx::f2_split(ptx::f2_mul(ptx::f2(x[0], x[1]), v0), x[0], x[1]);
+                        ptx::f2_split(ptx::f2_mul(ptx::f2(x[2], x[3]), v1), x[2], x[3]);
                         if constexpr (decltype(some)::value) {  // an unseen token's scale may be anything
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
@@ -420,7 +447,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
             ptx::tmem_st_wait();
             ptx::tc_fence_after();
             float *buf = reinterpret_cast<float *>(smem) + warp * 32 * kPitch;
-            const float up = BITS == 16 ? 1.0f : __uint_as_float(static_cast<unsigned>(127 + R) << 23);
+            const float up = BITS == 16 ? 1.0f : unit_of(-R);
             const float f = p.splits > 1 ? up : l == 0.0f ? 0.0f : up / l;
             const int64_t at = tok < 0 ? -1 : static_cast<int64_t>(sq.first + tok) * p.q_heads + head;
             const int64_t out_at =
@@ -623,7 +650,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
             // own block) in the other order: no two then meet in a bank.
             const int turn = D == 128 ? ch / (C::CPR / 2) : 0;
             const bool scales = lt >= kLoaders;
-            int R = -100;  // the unit of the values' scales, 2^R above every one so far
+            // The unit of the values' scales, 2^R above every one so far, of the tiles
+            // that all rows see alike: the context, and without a mask what lies before
+            // the block's first token.  Nothing of this kind comes after a tile of the
+            // other kind, where a row's unit is its own, over the tokens that it sees (a
+            // scale of another token would take the bits of its weights).
+            int R = -100;
+            const int alike = p.mask == nullptr ? row0 / p.group + 1 : 0;  // new tokens that all rows see
             auto issue = [&](int t) {
                 checked(raw_id, id);
                 pages(t + 1, raw_id);
@@ -663,14 +696,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
                     float *ks = reinterpret_cast<float *>(smem + C::OFF_META + stage * C::META), *vs = ks + kTok;
                     const float v0 = sc[kTok + lane], v1 = sc[kTok + 32 + lane];
                     const int e = top_exponent(__reduce_max_sync(0xffffffffu, max(finite_bits(v0), finite_bits(v1))));
-                    if (e > R) R = min(e + 1, 126);  // some room, so that it moves less often
-                    const float unit = __uint_as_float(static_cast<unsigned>(127 - R) << 23);
+                    const int j0 = (t0 + t) * kTok - sq.ctx;
+                    const bool own = j0 + kTok > alike;
+                    if (!own) R = raised(R, e);
+                    const float unit = own ? 1.0f : unit_of(R);
                     ks[lane] = sc[lane] * p.scale_log2, ks[32 + lane] = sc[32 + lane] * p.scale_log2;
                     vs[lane] = v0 * unit, vs[32 + lane] = v1 * unit;
                     if (lane == 0)
                         *reinterpret_cast<int4 *>(ks + 2 * kTok) =
-                            make_int4(static_cast<int>(live[0][0]), static_cast<int>(live[0][1]),
-                                      (t0 + t) * kTok - sq.ctx, R);
+                            make_int4(static_cast<int>(live[0][0]), static_cast<int>(live[0][1]), j0,
+                                      own ? kOwnUnit + e : R);
                     ptx::mbar_arrive(&bars->kv_full[stage]);
                     issue(t + C::RAWS - 1);
                     live[C::RAWS - 1][0] = live_of(id, t + C::RAWS - 1, 0);

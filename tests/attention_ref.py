@@ -88,9 +88,10 @@ def visible(mask, chain_i, n):
     return ((words[j // 32] >> (j % 32).astype(np.uint32)) & 1) > 0
 
 
-def attention(q, K, V, page_size, table, context, cu, mask, scale):
+def attention(q, K, V, page_size, table, context, cu, mask, scale, seen_only=False):
     """(out, lse, bound of out, bound of lse) in float64; rows of no sequence are NaN.
-    K, V float64 [pages, heads, page_size, D]."""
+    K, V float64 [pages, heads, page_size, D].  seen_only: a row's bound knows the tokens
+    that the row sees and no others."""
     q = q.astype(np.float64)
     n_rows, qh, D = q.shape
     heads = K.shape[1]
@@ -127,7 +128,7 @@ def attention(q, K, V, page_size, table, context, cu, mask, scale):
                 # values' scale over a power of two at most four times the largest
                 # scale among the sequence's rows, it is off by at most
                 # 2^-25 2^-10 4 max|v| a token, over the sum of the e's
-                most = np.abs(V[pg, h // G, pos % page_size]).max()
+                most = np.abs(v if seen_only else V[pg, h // G, pos % page_size]).max()
                 b_out[row, h] = (size * (HALF_F16 + 2 * d + (len(s) + 8) * 2.0 ** -23) * (1 + HALF_F16)
                                  + HALF_F16 * np.abs(out[row, h]) + TINY_F16
                                  + len(s) * most * 2.0 ** -33 / z)

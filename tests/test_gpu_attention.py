@@ -391,6 +391,71 @@ def test_unseen_rows_have_no_influence(bits, draft):
         assert not torch.isfinite(out[dev(seen)].float()).any()
 
 
+# (query heads a key head, new tokens, context, hint): a warp an item, a CTA an item, the stream
+# and its join; 16 and 32 rows by the warps, with and without splits; one and two blocks of
+# 128 rows by the tensor cores, with and without splits, several blocks of two
+FORMS = [(2, 3, 45, 0), (1, 8, 200, 200), (2, 4, 45, 1 << 16), (2, 8, 45, 0), (3, 5, 45, 1 << 17), (2, 16, 45, 0),
+         (2, 64, 45, 0), (1, 100, 2100, None), (2, 100, 45, 0), (4, 60, 2100, 1 << 17), (3, 200, 45, 0)]
+
+
+def place(c, b, i):
+    """Page and offset of new token i of sequence b."""
+    p = int(c.ctx[b]) + i
+    return int(c.table[b, p // c.page]), p % c.page
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,draft,ctx,hint", FORMS)
+@pytest.mark.parametrize("tree", [False, True])
+def test_unseen_value_scales_have_no_influence(bits, D, G, draft, ctx, hint, tree):
+    """A finite scale of any size at a token that a row does not see (a sibling branch, a
+    later token of a chunk, a slot that was never written) leaves that row as it was."""
+    c = Case(bits, D, 1, G, 32, [ctx, 9], [draft, 2], tree, seed=41, spread=0.3)
+    clean, clean_lse = c.run(hint)
+    checked()
+    bad = draft // 2  # a new token of the first sequence, unseen by the rows before it at least
+    if tree:
+        seen = (c.mask[:, bad // 32] >> np.uint32(bad % 32)) & 1 > 0
+        seen[c.cu[1]:] = False
+    else:
+        seen = np.zeros(c.rows, bool)
+        seen[bad:draft] = True
+    blind = dev(~seen)
+    page, at = place(c, 0, bad)
+    for scale in (1e3, 1e6, 1e9, 1e30, 3e38):
+        c.cache.v_scale[page, :, at] = scale
+        out, lse = c.run(hint)
+        checked()
+        assert torch.equal(out[blind], clean[blind]), scale
+        assert torch.equal(lse, clean_lse)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("G,draft,ctx,hint", FORMS)
+@pytest.mark.parametrize("tree", [False, True])
+def test_appended_values_of_any_size_beside_small_ones(bits, G, draft, ctx, hint, tree):
+    """Values around 1e-4 and, as a new token that some rows do not see, the largest fp16
+    ones, all through append: every row within the bound of the tokens that it sees."""
+    D = 128
+    c = Case(bits, D, 1, G, 32, [ctx], [draft], tree, seed=43)
+    n = ctx + draft
+    x = 1e-4 * c.r.standard_normal((n, 2, 1, D))
+    x[:, 0] *= 1e4
+    bad = ctx + draft // 2
+    x[bad, 1] = 65504 * np.sign(c.r.standard_normal((1, D)))
+    slots = [int(c.table[0, p // 32]) * 32 + p % 32 for p in range(n)]
+    X = dev(x.astype(np.float16))
+    c.cache.append(X[:, 0], X[:, 1], dev(np.array(slots, np.int64)))
+    out, lse = c.run(hint)
+    checked()
+    kv = [ref.values(b.cpu().numpy(), s.cpu().numpy(), bits)
+          for b, s in ((c.cache.k, c.cache.k_scale), (c.cache.v, c.cache.v_scale))]
+    o, z, bo, bz = ref.attention(c.q, *kv, 32, c.table, c.ctx, c.cu, c.mask, c.scale, seen_only=True)
+    within(out, o, bo, "out")
+    within(lse, z, bz, "lse")
+
+
 @pytest.mark.parametrize("draft", [8, 15, 90])
 def test_seen_infinity_in_fp16_values(draft):
     """An infinity in a value that some rows see: those rows get it, in its channel only."""
