@@ -533,6 +533,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
         // no such tokens).  They are looked at (checked) a tile later, when the loads
         // are long done: looked at at once they cost every tile a memory latency.
         constexpr int kNone = INT32_MIN;
+        // (reported by the last block, the one that comes to all of the sequence's tokens
+        // without a mask too)
+        const bool report = lt == 0 && row0 + QT * 128 >= rows;
         auto pages = [&](int t, int (&raw)[4]) {
 #pragma unroll
             for (int f = 0; f < 4; ++f) {
@@ -544,7 +547,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
 #pragma unroll
             for (int f = 0; f < 4; ++f) {
                 id[f] = static_cast<unsigned>(raw[f]) < static_cast<unsigned>(p.pages) ? raw[f] : -1;
-                if (id[f] < 0 && raw[f] != kNone && lt == 0 && rb == 0) atomicAdd(&g_attn_bad_index, 1u);
+                if (id[f] < 0 && raw[f] != kNone && report) atomicAdd(&g_attn_bad_index, 1u);
             }
         };
         auto id_of = [](const int (&id)[4], int f) { return f & 2 ? (f & 1 ? id[3] : id[2]) : (f & 1 ? id[1] : id[0]); };

@@ -592,6 +592,34 @@ def test_indices_out_of_range_are_reported():
     checked()
 
 
+@pytest.mark.parametrize("bits", BITS)
+@pytest.mark.parametrize("G,draft,ctx,hint", FORMS)
+@pytest.mark.parametrize("tree", [False, True])
+def test_a_bad_page_is_reported_by_every_form(bits, G, draft, ctx, hint, tree):
+    """A page number out of range, in the context or among the last new tokens of a chunk
+    of several row blocks: never used as an address, counted, and nothing to the rows
+    that see none of its tokens."""
+    c = Case(bits, 64, 1, G, 32, [ctx, 9], [draft, 2], tree, seed=47)
+    clean, clean_lse = c.run(hint)
+    checked()
+    keep = c.table.copy()
+    for column in (0, (ctx + draft - 1) // 32):
+        tokens = np.arange(32 * column, 32 * column + 32) - ctx  # as new tokens
+        sees = np.zeros(c.rows, bool)
+        for i in range(draft):
+            bits_of = ref.visible(None if c.mask is None else c.mask[i], i, draft)
+            sees[i] = (tokens < 0).any() or any(bits_of[j] for j in tokens if 0 <= j < draft)
+        for bad in (-1, c.cache.pages, 1 << 30):
+            c.table = keep.copy()
+            c.table[0, column] = bad
+            out, lse = c.run(hint)
+            assert q.quik_sync_check() == q.QUIK_ERR_INVALID_ARG, (column, bad)
+            assert torch.equal(out[dev(~sees)], clean[dev(~sees)])
+            assert torch.equal(lse[dev(~sees)], clean_lse[dev(~sees)])
+            assert torch.isfinite(out).all()
+    checked()
+
+
 @pytest.mark.parametrize("bits", [16, 4])
 @pytest.mark.parametrize("draft,hint", [(1, 0), (1, 1 << 16), (20, 0), (40, 0), (150, 0), (150, 1 << 16)])
 @pytest.mark.parametrize("tree", [False, True])
