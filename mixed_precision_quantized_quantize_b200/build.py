@@ -5,6 +5,9 @@
 nvcc cross-compiles without a GPU.  The CUDA runtime is linked statically and
 the driver API is reached through cudaGetDriverEntryPoint, so the library
 loads on a machine without a GPU (no symbol needs libcuda at load time).
+The library needs nvcc alone; the extension module _calls, which only the
+attention's Python calls use, also needs torch and a C++ compiler, and is left
+out where these are not there.
 """
 from __future__ import annotations
 
@@ -80,9 +83,19 @@ def build_calls(force: bool = False) -> str:
 
 def build(force: bool = False, verbose: bool = False, checks: bool = False) -> str:
     lib = LIB_CHECKED if checks else LIB
-    build_calls(force and not checks)
-    if not force and up_to_date(lib):
-        return lib
+    if force or not up_to_date(lib):
+        _compile(lib, verbose, checks)
+    if not checks:
+        try:
+            build_calls(force)
+        except (ImportError, OSError, subprocess.CalledProcessError) as e:
+            if os.path.exists(CALLS):  # of older sources: it must not meet the new library
+                os.remove(CALLS)
+            print(f"_calls is left out, the attention's Python calls will say so: {e}", file=sys.stderr)
+    return lib
+
+
+def _compile(lib: str, verbose: bool, checks: bool) -> None:
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [nvcc(), *NVCC_FLAGS, *(["-DQUIK_CHECKS"] if checks else []),
            "-I", os.path.join(ROOT, "include"), "-o", tmp, *sources()]
@@ -91,7 +104,6 @@ def build(force: bool = False, verbose: bool = False, checks: bool = False) -> s
         print(" ".join(cmd), file=sys.stderr)
     subprocess.check_call(cmd)
     os.replace(tmp, lib)
-    return lib
 
 
 if __name__ == "__main__":
