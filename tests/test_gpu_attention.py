@@ -654,6 +654,50 @@ def test_same_result_twice_and_on_another_stream():
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("bits", BITS)
+def test_raw_entry_points_give_the_same_bits(bits):
+    """The C calls with their structs, rows by their strides, on another stream."""
+    D, heads, G, n, page = 64, 2, 3, 70, 32
+    r = np.random.default_rng(53)
+    X = dev(r.standard_normal((n, (heads * G + 2 * heads) * D + 8)).astype(np.float16))
+    Y = X[:, :-8].unflatten(1, (-1, D))
+    Q, K, V = Y.split([heads * G, heads, heads], dim=1)
+    w = dev(np.abs(1 + 0.2 * r.standard_normal(D)).astype(np.float16))
+    cos, sin = (dev(t) for t in ref.tables(n, D))
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    slots = torch.arange(n, device="cuda")
+    table = torch.arange(3, dtype=torch.int32, device="cuda")[None]
+    ctx, cu = (torch.tensor(t, dtype=torch.int32, device="cuda") for t in ([n - 5], [n - 5, n]))
+    mask = torch.from_numpy(np.concatenate([np.zeros((n - 5, 1), np.uint32), ref.tree_mask(5, r)]).view(np.int32)).cuda()
+    a, b = (q.QuikKVCache.empty(3, heads, D, page, bits) for _ in "ab")
+    out, lse = (torch.zeros(s, dtype=t, device="cuda") for s, t in (((n, heads * G, D), torch.float16),
+                                                                  ((n, heads * G), torch.float32)))
+    qa, ka = q.qk_norm_rope(Q, K, w, None, 1e-5, cos, sin, pos)
+    a.append(ka, V, slots)
+    back = a.gather(slots)
+    q.tree_attention(qa, a, table, ctx, cu, 5, n - 5, mask=mask, out=out, lse=lse)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    qb, kb, back_k, back_v = (torch.empty_like(t) for t in (qa, ka, *back))
+    out_b, lse_b = torch.zeros_like(out), torch.zeros_like(lse)
+    shape = q.quik_heads(n, heads * G, heads, D, D, 0, n)
+    q.quik_qk_norm_rope(shape, Q, K, w, None, 1e-5, cos, sin, pos, qb, kb, stream=side)
+    q.quik_kv_append(q.quik_heads(n, 0, heads, D, 0, 0, 0), b.struct, kb, V, None, None, None, slots, stream=side)
+    q.quik_kv_gather(b.struct, slots, back_k, back_v, stream=side)
+    call = q.quik_attention(n, 1, heads * G, 5, 3, n - 5, 1, D ** -0.5)
+    ws = torch.empty(max(1, q.quik_attention_workspace_size(call, b.struct)), dtype=torch.uint8, device="cuda")
+    q.quik_tree_attention(call, b.struct, qb, table, ctx, cu, mask, out_b, lse_b, ws, stream=side)
+    side.synchronize()
+    checked()
+    for x, y in zip((qa, ka, *back, out, lse), (qb, kb, back_k, back_v, out_b, lse_b)):
+        assert torch.equal(x, y)
+    with pytest.raises(ValueError, match="heads of a token"):
+        q.quik_kv_gather(b.struct, slots, back_k.transpose(1, 2).contiguous().transpose(1, 2), back_v)
+    call.mask_words = 0  # fewer than five drafted tokens need
+    with pytest.raises(q.QuikError):
+        q.quik_tree_attention(call, b.struct, qb, table, ctx, cu, mask, out_b, lse_b, ws)
+
+
 def test_captured_and_replayed_with_other_lengths():
     """A captured call follows the lengths, pages and masks that its tensors hold
     at replay."""
