@@ -157,3 +157,137 @@ def test_a_warpgroup_meets_one_register_instruction():
     assert softmax % 128 == 0 and others % 128 == 0  # whole warpgroups on either side
     at_launch = 65536 // (softmax + others)
     assert softmax * sites[0][2] + others * sites[1][2] <= (softmax + others) * at_launch
+
+
+def run_out(n, stages, early, role, wait, seed):
+    """The same roles when wait number `wait` of `role` never comes to its end.  Once nobody
+    can go on, some role's wait runs out: it sets the CTA's abort flag, which all other
+    waits look at.  Returns the groups that wrote results, or None where the stalled wait
+    was never reached."""
+    rng = random.Random(seed)
+    full, empty = [Barrier(1) for _ in range(stages)], [Barrier(1) for _ in range(stages)]
+    s_full = [[Barrier(1), Barrier(1)] for _ in range(2)]
+    p_full = [[Barrier(1), Barrier(1)] for _ in range(2)]
+    pv, drain = [Barrier(1), Barrier(1)], Barrier(1)
+    holds, queue, wrote = {}, [], []
+
+    def loaders():
+        for t in range(n + early):
+            if early and t >= early:
+                full[(t - early) % stages].arrive()
+            if t < n:
+                if t >= stages and not (yield lambda t=t: empty[t % stages].passed(t // stages - 1)):
+                    break
+                assert t % stages not in holds, "a stage is filled while it is read"
+                holds[t % stages] = t
+                if not early:
+                    full[t % stages].arrive()
+
+    def values(t):
+        for g in range(2):
+            if not (yield lambda g=g: p_full[g][t & 1].passed(t >> 1)):
+                return False
+
+            def done(g=g):
+                assert holds[t % stages] == t
+                pv[g].arrive()
+                if g == 1:
+                    del holds[t % stages]
+                    empty[t % stages].arrive()
+            queue.append(done)
+        return True
+
+    def issuer():
+        alive = True
+        for t in range(n):
+            alive = yield lambda t=t: full[t % stages].passed(t // stages)
+            if not alive:
+                break
+            for g in range(2):
+                def done(t=t, g=g):
+                    assert holds[t % stages] == t
+                    s_full[g][t & 1].arrive()
+                queue.append(done)
+            if t > 0:
+                alive = yield from values(t - 1)
+            if not alive:
+                break
+        if alive and n > 0:
+            yield from values(n - 1)
+        # what was issued has to end before its memory is given back: this wait does not
+        # look at the flag
+        nonlocal draining
+        draining = True
+        queue.append(drain.arrive)
+        assert (yield lambda: drain.passed(0))
+        assert not queue
+
+    def softmax(g):
+        alive = True
+        for t in range(n):
+            alive = (yield lambda t=t: full[t % stages].passed(t // stages))
+            alive = alive and (yield lambda t=t: s_full[g][t & 1].passed(t >> 1))
+            if not alive:
+                break
+            if t > 0 and (rng.random() < 0.5 or t == n - 1):
+                alive = yield lambda t=t: pv[g].passed(t - 1)
+                if not alive:
+                    break
+            p_full[g][t & 1].arrive()
+        if alive and n > 0:
+            alive = yield lambda: pv[g].passed(n - 1)
+        if alive:
+            assert pv[g].phase == n  # every product is in
+            wrote.append(g)
+
+    roles, waits, reached, abort, draining = {}, {}, False, False, False
+
+    def step(name, make):
+        """Let a role go on; make(r): its next wait."""
+        nonlocal reached
+        r = roles[name][0]
+        try:
+            condition = make(r)
+        except StopIteration:
+            del roles[name]
+            return
+        waits[name] = waits.get(name, -1) + 1
+        if name == role and waits[name] == wait and not (name == "issuer" and draining):
+            reached = True
+            condition = lambda: False  # noqa: E731
+        roles[name][1] = condition
+
+    for name, r in (("loaders", loaders()), ("issuer", issuer()), ("softmax 0", softmax(0)), ("softmax 1", softmax(1))):
+        roles[name] = [r, None]
+        step(name, next)
+    while roles or queue:
+        ready = [(k, True) for k, (_, c) in roles.items() if c()]
+        if abort:
+            ready += [(k, False) for k, (_, c) in roles.items() if not c() and not (k == "issuer" and draining)]
+        moves = ready + ([("product", True)] if queue else [])
+        if not moves:
+            assert not abort, "a role waits on after the abort"
+            abort = True  # a wait has run out
+            continue
+        k, ok = rng.choice(moves)
+        if k == "product":
+            queue.pop(0)()
+        else:
+            step(k, lambda r: r.send(ok))
+    return wrote if reached else None
+
+
+@pytest.mark.parametrize("stages,early", [(4, 2), (3, 0)])
+@pytest.mark.parametrize("role", ["loaders", "issuer", "softmax 0", "softmax 1"])
+def test_a_wait_that_runs_out_ends_every_role(stages, early, role):
+    """Whichever wait stands still: every role ends, what was issued has ended before the
+    memory goes back, and a group that writes its rows has all of its products."""
+    met = 0
+    for n in (1, 2, 3, 7, 12):
+        for wait in range(3 * n + 1):
+            for seed in range(6):
+                wrote = run_out(n, stages, early, role, wait, seed)
+                if wrote is not None:
+                    met += 1
+                    assert not (role.startswith("softmax") and int(role[-1]) in wrote)
+    assert met > 50
