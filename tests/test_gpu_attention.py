@@ -698,6 +698,56 @@ def test_raw_entry_points_give_the_same_bits(bits):
         q.quik_tree_attention(call, b.struct, qb, table, ctx, cu, mask, out_b, lse_b, ws)
 
 
+class Guarded:
+    """Tensors with 4 KB of a pattern before and after each."""
+
+    def __init__(self):
+        self.all = []
+
+    def __call__(self, shape, dtype):
+        n = int(np.prod(shape)) * torch.empty(0, dtype=dtype).element_size()
+        buf = torch.full((4096 + -(-n // 16) * 16 + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        self.all.append((buf, n))
+        return buf[4096:4096 + n].view(dtype).view(shape)
+
+    def untouched(self):
+        return all((b[:4096] == 0xA5).all() and (b[4096 + n:] == 0xA5).all() for b, n in self.all)
+
+
+@pytest.mark.parametrize("bits", BITS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,draft,ctx,hint", FORMS)
+def test_guards_around_every_output_are_untouched(bits, D, G, draft, ctx, hint):
+    """Guard bytes around the cache, its scales, the outputs and the workspace of one step:
+    norm and rotation, append into all of the cache, read-back, attention."""
+    heads, page, g = 3, 16, Guarded()
+    n = ctx + draft
+    pages = -(-n // page)
+    r = np.random.default_rng(59)
+    X = dev(r.standard_normal((n, heads * G + 2 * heads, D)).astype(np.float16))
+    Q, K, V = X.split([heads * G, heads, heads], dim=1)
+    row, dtype = {16: (D, torch.float16), 8: (D, torch.int8), 4: (D // 2, torch.uint8)}[bits]
+    cache = q.QuikKVCache(*(g((pages, heads, page, row), dtype) for _ in "kv"),
+                          *((g((pages, heads, page), torch.float32) for _ in "kv") if bits < 16 else (None, None)))
+    cos, sin = (dev(t) for t in ref.tables(n, D))
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    qo, ko = g((n, heads * G, D), torch.float16), g((n, heads, D), torch.float16)
+    q.qk_norm_rope(Q, K, None, None, 1e-5, cos, sin, pos, q_out=qo, k_out=ko)
+    slots = torch.arange(n, device="cuda")
+    cache.append(ko, V, slots)
+    cache.gather(slots, *(g((n, heads, D), torch.float16) for _ in "kv"))
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    context, cu = (torch.tensor(t, dtype=torch.int32, device="cuda") for t in ([ctx], [0, draft]))
+    out, lse = g((draft, heads * G, D), torch.float16), g((draft, heads * G), torch.float32)
+    for words in (0, -(-draft // 32)):
+        call = q.quik_attention(draft, 1, heads * G, draft, pages, ctx if hint is None else hint, words, D ** -0.5)
+        mask = dev(ref.tree_mask(draft, r, words).view(np.int32)) if words else None
+        ws = g((q.quik_attention_workspace_size(call, cache.struct),), torch.uint8)
+        q.quik_tree_attention(call, cache.struct, qo[ctx:], table, context, cu, mask, out, lse, ws)
+    checked()
+    assert g.untouched()
+
+
 def test_captured_and_replayed_with_other_lengths():
     """A captured call follows the lengths, pages and masks that its tensors hold
     at replay."""
