@@ -475,7 +475,12 @@ QUIK_API quik_status quik_kv_gather(const quik_kv_cache *cache, int32_t tokens,
  *     lse = ln sum_j exp(scale * (q . k_j))
  * Scores, softmax and sums are fp32; p is rounded to fp16 before its product
  * with the stored values (codes, in the quantised types: the values' scale is
- * part of p then).  A row that sees nothing gives zeros and lse = -infinity.
+ * part of p then, over a power of two above the scales that the row sees).
+ * Calls over short contexts with up to 8 rows a key head take the part of
+ * these roundings that a row's weights have in common out again; in other
+ * calls a row that sees two or three tokens keeps it (up to 2^-11 of the
+ * output beside the output's own rounding).  A row that sees nothing gives
+ * zeros and lse = -infinity.
  * A token that a row does not see has no influence on it, whatever its cache
  * row holds.
  *   q [tokens, q_heads, head_dim] fp16, row stride q_stride; out alike
@@ -484,8 +489,10 @@ QUIK_API quik_status quik_kv_gather(const quik_kv_cache *cache, int32_t tokens,
  *   tree_mask uint32 [tokens, mask_words], mask_words >= max_tokens / 32
  *   rounded up (NULL: mask_words is not used)
  *   lse fp32 [tokens, q_heads] or NULL
- *   max_tokens: the largest n_b; max_context: the largest context[b], a hint
- *   that only chooses how the work is split (any value is right)
+ *   max_tokens: the largest n_b; 0 says that no sequence has any: there is no
+ *   launch then, as without sequences, and the lengths are not looked at
+ *   max_context: the largest context[b], a hint that only chooses how the work
+ *   is split (any value is right)
  * Rows of out and lse before cu_tokens[0] and from cu_tokens[sequences] on
  * are left as they were.  Positions are read in place: a page number outside
  * [0, pages) is never used as an address (its tokens are unseen), a sequence

@@ -720,7 +720,7 @@ def tree_attention(q: torch.Tensor, cache: QuikKVCache, page_table: torch.Tensor
     [tokens, words]: bit j of a row, the new token j it sees (None: a chain).  scale defaults to
     head_dim ** -0.5.  Returns out [tokens, q_heads, head_dim], with return_lse (out, lse fp32
     [tokens, q_heads]).  Rows that belong to no sequence are left as they were (in new tensors:
-    undefined)."""
+    undefined); with max_tokens 0 those are all rows, whatever cu_tokens holds."""
     if stream is not None:
         with _on(stream, q):
             return tree_attention(q, cache, page_table, context, cu_tokens, max_tokens, max_context, mask, scale,

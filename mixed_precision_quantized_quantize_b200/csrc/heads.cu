@@ -16,9 +16,9 @@
 // (two fp32 an instruction).  Norm and rotation of 2048 x 64 heads of 128: 18.6 us
 // with eight channels a lane and the partner's shuffled in, 15.3 with two runs of
 // four, 14.6 with two runs of eight and four CTAs an SM (10.4 by the bytes).
-// Appends of 2048 x 32 heads of 128 in fp16 take 14.1 us (10.4 by the bytes), of
-// 4093 x 8 in INT8 8.5 and read back 5.7 (6.7 for both), of 4096 x 32 in INT4 27.8
-// and read back 15.9 (23.5 for both).
+// Appends of 2048 x 32 heads of 128 in fp16 take 14.4 us (10.4 by the bytes) and
+// read back 12.9 (10.2), of 4093 x 8 in INT8 8.4 and read back 6.1 (6.7 for both),
+// of 4096 x 32 in INT4 27.7 and read back 17.5 (23.5 for both).
 #include "quik_internal.h"
 #include "sm100.cuh"
 

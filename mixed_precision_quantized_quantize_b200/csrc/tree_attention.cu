@@ -557,10 +557,10 @@ __global__ void __launch_bounds__(C::NW * 32) tree_attention_kernel(const Params
 // products, accumulators and exponentials.  P^T turns from the accumulators'
 // layout into the second product's operand by movmatrix.
 //
-// A token over 200 of INT8, 32 heads: 6.4 us; one of 16 sequences over up to 2048 of
-// INT4, 32 heads: 37 us with the join (16.9 by the bytes; the conversion of codes
-// keeps the ALU half busy at 16 warps an SM); one over 65536 of fp16, 64 / 8 heads:
-// 54 us (40.9 by the bytes).
+// A token over 200 of INT8, 32 heads: 6.4 to 6.6 us; one of 16 sequences over up to 2048
+// of INT4, 32 heads: 37 us with the join (16.9 by the bytes; the conversion of codes
+// keeps the ALU half busy at 16 warps an SM); one over 65536, 64 / 8 heads: fp16 54 us
+// (40.9 by the bytes), INT8 39 (21.1), INT4 32 (10.9).
 //
 // Short contexts: see FewMode.  Otherwise the work, tiles of all sequences, key heads
 // and blocks of 8 rows one after the other, is cut into equal runs, one a warp, whatever the sequences'
@@ -1444,12 +1444,12 @@ FewWarps few_warps(int head_dim) {
 // Up to eight rows: who takes an item of at most `tiles` tiles.  Times are counted
 // in tiles of 128 channels, about 0.8 us for a warp.  Measured, us, one token of
 // each sequence over (a warp an item / a CTA an item / the stream and its join):
-//     1 sequence, 32 heads of 128, INT8:     100 tokens 10.0 / 5.0 / -
-//         250 tokens - / 6.2 / 7.8, 600 tokens - / 9.3 / 8.7
-//     16 sequences, 32 heads of 128, fp16:   60 tokens 7.9 / 15.2 / -
-//         150 tokens - / 18.8 / 13.6
-//     128 sequences, 32 / 8 heads of 64, INT4: 60 tokens 5.9 / 8.4 / -
-//         250 tokens - / 12.7 / 20.8, 900 tokens - / 27.3 / 34.0
+//     1 sequence, 32 heads of 128, INT8:     100 tokens 10.3 / 5.1 / 7.8
+//         250 tokens 16.8 / 6.4 / 8.0, 600 tokens 33.7 / 9.6 / 8.8
+//     16 sequences, 32 heads of 128, fp16:   60 tokens 8.1 / 16.2 / 10.5
+//         150 tokens 13.9 / 21.1 / 14.7
+//     128 sequences, 32 / 8 heads of 64, INT4: 60 tokens 6.3 / 9.2 / 15.7
+//         250 tokens 12.6 / 14.1 / 21.2, 900 tokens 35.1 / 31.9 / 36.6
 FewMode few_mode(const AttentionArgs &a, int64_t items, int64_t tiles, const FewWarps &w) {
     const int64_t resident = static_cast<int64_t>(sm_count()) * w.sm / w.cta, waves = (items + resident - 1) / resident;
     if (tiles <= 4) return waves == 1 ? kGroup : kWarp;
@@ -1466,10 +1466,11 @@ FewMode few_mode(const AttentionArgs &a, int64_t items, int64_t tiles, const Few
 // tcgen05 form, whose tiles take as long for one row as for 128 and whose CTAs
 // start slowly, but which reads and converts a tile once for all of them.  Both
 // measured, 8 sequences of 4096 tokens, 8 key heads of 128, us (warps / tcgen05):
-//     16 rows   INT4 27.1 / 40.7   INT8 31.3 / 37.7   fp16 41.7 / 34.3
-//     32 rows   INT4 43.5 / 41.1   INT8 46.6 / 37.9   fp16 47.1 / 34.6
-// 32 sequences of 300 tokens, 32 rows: INT8 16.5 / 23.1.  Heads of 64, 64 rows:
-// 2 sequences of 300 tokens INT8 9.3 / 9.9, 8 of 4096 tokens 50.0 / 36.1.
+//     16 rows   INT4 28.3 / 41.9   INT8 33.9 / 39.3   fp16 44.2 / 35.2
+//     32 rows   INT4 44.3 / 42.2   INT8 48.6 / 39.3   fp16 50.6 / 35.5
+//     64 rows   INT4 66.8 / 42.6   INT8 71.5 / 39.8   fp16 74.4 / 36.0
+// 32 sequences of 300 tokens, 32 rows: INT8 16.9 / 23.4.  Heads of 64, 64 rows:
+// 2 sequences of 300 tokens INT8 9.4 / 10.2, 8 of 4096 tokens 50.0 / 37.2.
 int narrow_rows(const AttentionArgs &a) {
     const bool long_context = a.max_context >= 2048;
     if (a.cache.head_dim == 64) return long_context ? 32 : 64;

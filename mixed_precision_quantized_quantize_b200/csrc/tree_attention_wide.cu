@@ -26,8 +26,10 @@
 // special-function units for both), 100 for P.  The products take 900 and the
 // conversion 1800, beside them.  Around the tiles a CTA takes 6000 cycles to its
 // first S and 5000 for its results.  64 drafted tokens over 8 x 4096 of INT8,
-// 32 / 8 heads of 128: 55 us with the join, 17.4 by the products' rate.  A chunk of
-// 2048 tokens of a prompt, fp16: 95 us.  Tried and slower:
+// 32 / 8 heads of 128: 55 to 56 us with the join, 17.4 by the products' rate.  A chunk
+// of 2048 tokens of a prompt, the same heads: fp16 91 us, INT8 76, INT4 78 (21.3 by the
+// products' rate; quantised rows skip the masks on tiles that all rows see whole).
+// Tried and slower:
 // two threads a row (more warps, the same time: 60.5 us), one row block by two
 // groups that take tiles in turn (64 rows fp16 55.0 against 38.0 us), pieces by
 // each sequence's own length (60.7 against 58.3 us: finding the place costs more).
@@ -148,7 +150,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_attention_wide_kernel(cons
     // too: the products' descriptors and loop then live in uniform registers)
     const int lane = threadIdx.x % 32, warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);
     const int split = blockIdx.x % p.splits;
-    const int rb = p.row_blocks - 1 - blockIdx.x / p.splits;  // (the blocks that see most start first)
+    const int rb = p.row_blocks - 1 - blockIdx.x / p.splits;  // (a key head's blocks that see most start first)
     const int h = blockIdx.y, b = blockIdx.z;
     Seq sq = sequence(p, b, blockIdx.x == 0 && h == 0 && threadIdx.x == 0);
     const int rows = sq.n * p.group, row0 = rb * QT * 128;
