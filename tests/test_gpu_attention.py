@@ -432,6 +432,27 @@ def test_unseen_value_scales_have_no_influence(bits, D, G, draft, ctx, hint, tre
 
 
 @pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("most", [60, 230])
+def test_unseen_value_scales_in_many_short_sequences(bits, D, most):
+    """The same where a warp takes an item whole, or one stream crosses many of them: the
+    second of three drafted tokens in each of 200 sequences."""
+    r = np.random.default_rng(most)
+    c = Case(bits, D, 4, 2, 32, r.integers(0, most, 200).tolist(), [3] * 200, True, seed=61)
+    clean, _ = c.run()
+    seen = dev((c.mask[:, 0] >> 1) & 1 > 0)
+    for b in range(200):
+        page, at = place(c, b, 1)
+        c.cache.v_scale[page, :, at] = (1e3, 1e9, 1e30)[b % 3]
+    for hint in (None, 1 << 14):
+        out, _ = c.run(hint)
+        checked()
+        if hint is None:
+            assert torch.equal(out[~seen], clean[~seen])
+        assert torch.allclose(out[~seen].float(), clean[~seen].float(), rtol=8 * ref.HALF_F16, atol=2e-3)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
 @pytest.mark.parametrize("G,draft,ctx,hint", FORMS)
 @pytest.mark.parametrize("tree", [False, True])
 def test_appended_values_of_any_size_beside_small_ones(bits, G, draft, ctx, hint, tree):
